@@ -15,6 +15,11 @@ from .binding import (  # noqa: F401
     nv_gather_qmm_workspace_size,
     nv_dequantize_affine,
     nv_dequantize_fp,
+    nv_kv_attention,
+    nv_kv_attention_workspace_size,
+    nv_kv_dequantize,
+    nv_kv_quantize,
+    nv_moe_route,
     nv_moe_swiglu,
     nv_moe_swiglu_workspace_size,
     nv_pipeline_error,

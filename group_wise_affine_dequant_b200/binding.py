@@ -22,6 +22,8 @@ NV_ROW_INDEPENDENT_ROWS = 8
 NV_FLAG_EXPERT_OUT_OF_RANGE = 0x1
 NV_FLAG_NOT_SORTED = 0x2
 NV_FLAG_TOKEN_OUT_OF_RANGE = 0x4
+NV_FLAG_PAGE_OUT_OF_RANGE = 0x8
+NV_FLAG_BAD_LENGTH = 0x10
 
 # Every entry point declared in include/nvq.h.
 EXPORTS = ("nv_status_string", "nv_quantize_affine", "nv_dequantize_affine", "nv_qmm",
@@ -29,16 +31,22 @@ EXPORTS = ("nv_status_string", "nv_quantize_affine", "nv_dequantize_affine", "nv
            "nv_gather_qmm_workspace_size", "nv_gather_mm",
            "nv_gather_qmm", "nv_gather_qmm_flags", "nv_pipeline_error", "nv_pipeline_selftest",
            "nv_last_cuda_error",
-           "nv_gather_qmm_noalloc", "nv_quantize_fp", "nv_dequantize_fp", "nv_qmm_fp")
+           "nv_gather_qmm_noalloc", "nv_quantize_fp", "nv_dequantize_fp", "nv_qmm_fp",
+           "nv_moe_route", "nv_kv_quantize", "nv_kv_dequantize", "nv_kv_attention",
+           "nv_kv_attention_workspace_size")
 NV_FP_MODES = {"mxfp4": 1, "mxfp8": 2, "nvfp4": 3}
 _FP_GROUP = {"mxfp4": 32, "mxfp8": 32, "nvfp4": 16}
 _FP_BITS = {"mxfp4": 4, "mxfp8": 8, "nvfp4": 4}
+
+NV_KV_INT8, NV_KV_E4M3 = 1, 2
+_KV_MODES = {torch.int8: NV_KV_INT8, torch.float8_e4m3fn: NV_KV_E4M3}
+_ROUTE_SCORES = {"softmax": 0, "sigmoid": 1}
 
 _DT = {torch.float32: NV_F32, torch.bfloat16: NV_BF16}
 _LOCK = threading.Lock()
 _LIB = None
 
-_p, _i64, _i, _sz = C.c_void_p, C.c_int64, C.c_int, C.c_size_t
+_p, _i64, _i, _sz, _f = C.c_void_p, C.c_int64, C.c_int, C.c_size_t, C.c_float
 
 
 class NvqError(RuntimeError):
@@ -105,6 +113,18 @@ def lib():
             L.nv_dequantize_fp.restype = _i
             L.nv_qmm_fp.argtypes = [_p, _i, _i64, _i64, _i64, _p, _p, _i, _p, _p]
             L.nv_qmm_fp.restype = _i
+            L.nv_moe_route.argtypes = [_p, _i, _i64, _i64, _p, _i, _i, _i, _i, _i, _i, _f, _p, _p, _p]
+            L.nv_moe_route.restype = _i
+            cache, steps = [_p, _p, _p, _p, _i, _i64, _i, _i, _i], [_p, _i64, _p, _p, _i64]
+            L.nv_kv_quantize.argtypes = [_p, _p, _i64, _i64, _i, _i64, *cache, *steps, _p, _p]
+            L.nv_kv_quantize.restype = _i
+            L.nv_kv_dequantize.argtypes = [*cache, *steps, _i, _i64, _p, _p, _p, _p]
+            L.nv_kv_dequantize.restype = _i
+            L.nv_kv_attention.argtypes = [_p, _i64, _i, _i64, _i, *cache, *steps, _f, _i, _i, _i64, _p,
+                                          _sz, _p, _p, _p]
+            L.nv_kv_attention.restype = _i
+            L.nv_kv_attention_workspace_size.argtypes = [_i, _i64, _i, _i, _i, _i, _i64, _i64, _i64]
+            L.nv_kv_attention_workspace_size.restype = _sz
             _LIB = L
         return _LIB
 
@@ -459,3 +479,188 @@ def nv_qmm_fp(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, mode: 
                          y.data_ptr(), _stream(stream))
     _check("nv_qmm_fp", st)
     return y
+
+
+class _On:
+    """Makes the tensors' device current for a call, where it is not already, and
+    gives the stream the call goes to: the given one, else that device's current one."""
+
+    __slots__ = ("guard", "stream")
+
+    def __init__(self, device: torch.device, stream):
+        self.guard = None
+        if device.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(device)
+        self.stream = stream
+
+    def __enter__(self) -> int:
+        if self.guard is not None:
+            self.guard.__enter__()
+        return _stream(self.stream)
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def nv_moe_route(logits: torch.Tensor, topk: int, score: str = "softmax",
+                 bias: torch.Tensor | None = None, groups: int = 1, topk_groups: int | None = None,
+                 group_top: int = 1, renormalize: bool = True, scale: float = 1.0,
+                 ids: torch.Tensor | None = None, weights: torch.Tensor | None = None, stream=None):
+    """(ids int32 [T, topk], weights fp32 [T, topk]) of router logits [T, E]: what
+    nv_moe_swiglu takes as ids and rw. score 'softmax' or 'sigmoid'; bias fp32 [E]
+    is added for the choice only; with groups > 1 only the topk_groups best groups
+    are chosen from (a group's score: its group_top = 1 or 2 largest, summed)."""
+    _dev(logits, "logits")
+    if logits.dim() != 2 or score not in _ROUTE_SCORES:
+        raise ValueError(f"logits must be [T, E] and score one of {sorted(_ROUTE_SCORES)}")
+    T, E = logits.shape
+    device = logits.device
+    if bias is not None:
+        _dev(bias, "bias")
+        if bias.dtype != torch.float32 or bias.numel() != E or bias.device != device:
+            raise ValueError("bias must be fp32 [E] on the logits' device")
+    outs = []
+    for t, dtype, name in ((ids, torch.int32, "ids"), (weights, torch.float32, "weights")):
+        if t is None:
+            t = torch.empty(T, max(topk, 0), dtype=dtype, device=device)
+        else:
+            _dev(t, name)
+            if tuple(t.shape) != (T, topk) or t.dtype != dtype or t.device != device:
+                raise ValueError(f"{name} must be {dtype} [T, topk] on the logits' device")
+        outs.append(t)
+    with _On(device, stream) as s:
+        st = lib().nv_moe_route(logits.data_ptr(), _DT.get(logits.dtype, -1), T, E, _ptr(bias),
+                                _ROUTE_SCORES[score], groups, groups if topk_groups is None else topk_groups,
+                                group_top, topk, int(renormalize), scale, outs[0].data_ptr(),
+                                outs[1].data_ptr(), s)
+    _check("nv_moe_route", st)
+    return outs[0], outs[1]
+
+
+def _kv_args(k_codes, k_scales, v_codes, v_scales, pages, starts, lens, flags):
+    """The cache's and the step descriptor's arguments as the C calls take them,
+    after the checks that need shapes: (cache, steps, flags pointer, H, D, device)."""
+    device = k_codes.device
+    for t, n in ((k_codes, "k_codes"), (k_scales, "k_scales"), (v_codes, "v_codes"),
+                 (v_scales, "v_scales"), (pages, "pages"), (starts, "starts"), (lens, "lens")):
+        if not t.is_cuda or not t.is_contiguous() or t.device != device:
+            raise ValueError(f"{n} must be a contiguous CUDA tensor on the cache's device")
+    if k_codes.dim() != 4 or k_codes.shape != v_codes.shape or k_codes.dtype != v_codes.dtype:
+        raise ValueError("k_codes and v_codes must be [P, H, block, D] alike")
+    P, H, block, D = k_codes.shape
+    mode = _KV_MODES.get(k_codes.dtype)
+    if mode is None:
+        raise ValueError("codes must be torch.int8 or torch.float8_e4m3fn")
+    for t, n in ((k_scales, "k_scales"), (v_scales, "v_scales")):
+        if t.dtype != torch.float32 or t.dim() != 2 or t.shape[0] != P or t.shape[1] != H:
+            raise ValueError(f"{n} must be fp32 [P, H]")
+    S = lens.shape[0] if lens.dim() == 1 else -1
+    if pages.dim() != 2 or pages.shape[0] != S or starts.dim() != 1 or starts.shape[0] != S + 1:
+        raise ValueError("pages [S, max_pages], starts [S + 1] and lens [S] expected")
+    if pages.dtype != torch.int32 or starts.dtype != torch.int32 or lens.dtype != torch.int32:
+        raise ValueError("pages, starts and lens must be int32")
+    if flags is not None and (not flags.is_cuda or flags.dtype != torch.int32 or flags.numel() < 1 or
+                              flags.device != device):
+        raise ValueError("flags must be an int32 CUDA tensor on the cache's device")
+    return ((k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), mode, P,
+             H, block, D),
+            (pages.data_ptr(), pages.shape[1], starts.data_ptr(), lens.data_ptr(), S), _ptr(flags), H, D,
+            device)
+
+
+def _kv_rows(t: torch.Tensor, name: str, heads: int, D: int, device) -> int:
+    """Row stride of a step's tensor [rows, heads, D]: dense heads, any distance between rows."""
+    if not t.is_cuda or t.device != device or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != D:
+        raise ValueError(f"{name} must be [rows, {heads}, {D}] on the cache's device")
+    rows, dense = t.shape[0], heads * D
+    row, head, last = t.stride()
+    if (last != 1 and D > 1) or (head != D and heads > 1):
+        raise ValueError(f"the heads of a row of {name} must be dense")
+    return row if rows > 1 else dense
+
+
+def nv_kv_quantize(k: torch.Tensor, v: torch.Tensor, k_codes: torch.Tensor, k_scales: torch.Tensor,
+                   v_codes: torch.Tensor, v_scales: torch.Tensor, pages: torch.Tensor,
+                   starts: torch.Tensor, lens: torch.Tensor, flags: torch.Tensor | None = None,
+                   stream=None) -> None:
+    """Write a step's keys and values [rows, H, D] (rows may be strided) into the
+    paged 8-bit cache: codes int8 or float8_e4m3fn [P, H, block, D], scales fp32
+    [P, H]. Rows starts[s] .. starts[s + 1] are the last tokens of sequence s,
+    lens[s] its length with them, pages[s, j] the page of its j-th block."""
+    cache, steps, fl, H, D, device = _kv_args(k_codes, k_scales, v_codes, v_scales, pages, starts, lens, flags)
+    ks, vs = _kv_rows(k, "k", H, D, device), _kv_rows(v, "v", H, D, device)
+    if k.shape != v.shape or k.dtype != v.dtype:
+        raise ValueError("k and v must be alike")
+    with _On(device, stream) as s:
+        st = lib().nv_kv_quantize(k.data_ptr(), v.data_ptr(), ks, vs, _DT.get(k.dtype, -1), k.shape[0],
+                                  *cache, *steps, fl, s)
+    _check("nv_kv_quantize", st)
+
+
+def nv_kv_dequantize(k_codes: torch.Tensor, k_scales: torch.Tensor, v_codes: torch.Tensor,
+                     v_scales: torch.Tensor, pages: torch.Tensor, starts: torch.Tensor,
+                     lens: torch.Tensor, rows: int, dtype=torch.bfloat16, out=None,
+                     flags: torch.Tensor | None = None, stream=None):
+    """(k, v) [rows, H, D]: the last starts[s + 1] - starts[s] tokens of every
+    sequence, read back (all of them where starts is the running sum of lens).
+    out: a pair of tensors to write to; rows of no sequence are left as they were."""
+    cache, steps, fl, H, D, device = _kv_args(k_codes, k_scales, v_codes, v_scales, pages, starts, lens, flags)
+    if out is None:
+        k = torch.empty(rows, H, D, dtype=dtype, device=device)
+        v = torch.empty(rows, H, D, dtype=dtype, device=device)
+    else:
+        k, v = out
+        for t, n in ((k, "out[0]"), (v, "out[1]")):
+            _dev(t, n)
+            if tuple(t.shape) != (rows, H, D) or t.dtype != dtype or t.device != device:
+                raise ValueError(f"{n} must be {dtype} [rows, H, D] on the cache's device")
+    with _On(device, stream) as s:
+        st = lib().nv_kv_dequantize(*cache, *steps, _DT.get(dtype, -1), rows, k.data_ptr(), v.data_ptr(), fl, s)
+    _check("nv_kv_dequantize", st)
+    return k, v
+
+
+def nv_kv_attention_workspace_size(rows: int, Hq: int, H: int, block: int, D: int, max_pages: int, S: int,
+                                   max_q: int = 0, dtype=torch.bfloat16) -> int:
+    return int(lib().nv_kv_attention_workspace_size(_DT.get(dtype, -1), rows, Hq, H, block, D, max_pages, S,
+                                                    max_q))
+
+
+def nv_kv_attention(q: torch.Tensor, k_codes: torch.Tensor, k_scales: torch.Tensor,
+                    v_codes: torch.Tensor, v_scales: torch.Tensor, pages: torch.Tensor,
+                    starts: torch.Tensor, lens: torch.Tensor, scale: float | None = None,
+                    causal: bool = True, window: int = 0, max_q: int = 0,
+                    workspace: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                    flags: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Attention of a step's queries [rows, Hq, D] (rows may be strided) over the
+    paged 8-bit cache, which holds the step's own keys and values already. scale
+    defaults to D ** -0.5; window > 0 limits a causal row to its last `window`
+    tokens; max_q is the largest number of rows of one sequence, if known.
+    Returns out [rows, Hq, D]; rows of no sequence are left as they were."""
+    cache, steps, fl, H, D, device = _kv_args(k_codes, k_scales, v_codes, v_scales, pages, starts, lens, flags)
+    if q.dim() != 3:
+        raise ValueError("q must be [rows, Hq, D]")
+    rows, Hq = q.shape[0], q.shape[1]
+    qs = _kv_rows(q, "q", Hq, D, device)
+    if out is None:
+        out = torch.empty(rows, Hq, D, dtype=q.dtype, device=device)
+    else:
+        _dev(out, "out")
+        if out.shape != q.shape or out.dtype != q.dtype or out.device != device:
+            raise ValueError("out must be dense and like q")
+    L, dt = lib(), _DT.get(q.dtype, -1)
+    if workspace is None:
+        need = L.nv_kv_attention_workspace_size(dt, rows, Hq, H, cache[7], D, steps[1], steps[4], max_q)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    else:
+        _dev(workspace, "workspace")
+    wp, wb = (None, 0) if workspace is None else (workspace.data_ptr(),
+                                                  workspace.numel() * workspace.element_size())
+    with _On(device, stream) as s:
+        st = L.nv_kv_attention(q.data_ptr(), qs, dt, rows, Hq, *cache, *steps,
+                               D ** -0.5 if scale is None else scale, int(causal), window, max_q, wp, wb,
+                               out.data_ptr(), fl, s)
+    _check("nv_kv_attention", st)
+    return out

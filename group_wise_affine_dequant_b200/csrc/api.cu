@@ -7,6 +7,7 @@
 
 #include "common.cuh"
 #include "kernels.cuh"
+#include "kv.cuh"
 #include "tc.cuh"
 
 namespace {
@@ -37,6 +38,38 @@ nv_status from_cuda(cudaError_t e) {
     if (e == cudaSuccess) return NV_OK;
     t_last_cuda_error = e;
     return NV_ERR_CUDA;
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Checks shared by the key/value cache calls: sizes first (NV_OK and *empty for
+// a call with nothing to do), then pointers.
+nv_status check_kv(nv_dtype dt, int64_t rows, const nvq::KvCache& c, int64_t S, int64_t max_pages,
+                   bool* empty) {
+    if (!valid_dtype(dt)) return NV_ERR_UNSUPPORTED;
+    if (c.mode != NV_KV_INT8 && c.mode != NV_KV_E4M3) return NV_ERR_INVALID_ARG;
+    if (rows < 0 || rows > 0x7FFFFFFF || S < 0 || S > 0xFFFFFF || max_pages < 0 ||
+        max_pages > 0x7FFFFFFF || c.P < 0 || c.P > 0x7FFFFFFF || c.H < 1 || c.H > 1024 || c.D < 1 ||
+        c.block < 1)
+        return NV_ERR_INVALID_ARG;
+    if (c.D % 16 || c.D > 256 || (c.block != 16 && c.block != 32 && c.block != 64 && c.block != 128))
+        return NV_ERR_UNSUPPORTED;
+    *empty = rows == 0 || S == 0;
+    return NV_OK;
+}
+nv_status check_kv_pointers(const nvq::KvCache& c, const nvq::KvSteps& st) {
+    if (!c.k_codes || !c.k_scales || !c.v_codes || !c.v_scales || !st.pages || !st.starts || !st.lens)
+        return NV_ERR_INVALID_ARG;
+    if (!aligned16(c.k_codes) || !aligned16(c.v_codes)) return NV_ERR_INVALID_ARG;
+    for (const void* p : {static_cast<const void*>(c.k_scales), static_cast<const void*>(c.v_scales),
+                          static_cast<const void*>(st.pages), static_cast<const void*>(st.starts),
+                          static_cast<const void*>(st.lens), static_cast<const void*>(st.flags)})
+        if (!aligned4(p)) return NV_ERR_INVALID_ARG;
+    return NV_OK;
+}
+// A row stride in elements: the heads fit and every row starts on 16 bytes.
+bool valid_stride(int64_t stride, int64_t least, nv_dtype dt) {
+    return stride >= least && stride < (int64_t(1) << 40) && stride % (dt == NV_F32 ? 4 : 8) == 0;
 }
 
 int sm_count() {
@@ -284,6 +317,93 @@ nv_status nv_gather_mm(const void* x, nv_dtype dt, int64_t x_rows, int64_t K,
     if (N == 0) return NV_OK;
     return from_cuda(nvq::launch_tc_gather_mm(x, x_rows, K, lhs_idx, ws.perm, ws.offsets, E, N, w,
                                               y, s, sm_count()));
+}
+
+nv_status nv_moe_route(const void* logits, nv_dtype dt, int64_t T, int64_t E, const float* bias,
+                       int score_fn, int groups, int topk_groups, int group_top, int topk,
+                       int renormalize, float scale, uint32_t* ids, float* weights,
+                       nv_stream_t stream) {
+    if (!valid_dtype(dt)) return NV_ERR_UNSUPPORTED;
+    if (T < 0 || T > 0x7FFFFFFF || E < 1 || (score_fn != 0 && score_fn != 1) || groups < 1 || E % groups ||
+        topk_groups < 1 || topk_groups > groups || (group_top != 1 && group_top != 2) || topk < 1 ||
+        topk > 64 || topk > topk_groups * (E / groups))
+        return NV_ERR_INVALID_ARG;
+    if (E > nvq::kMaxExperts) return NV_ERR_UNSUPPORTED;
+    if (T == 0) return NV_OK;
+    if (!logits || !ids || !weights || !aligned16(logits) || !aligned4(bias) || !aligned4(ids) ||
+        !aligned4(weights))
+        return NV_ERR_INVALID_ARG;
+    return from_cuda(nvq::launch_moe_route(logits, dt, T, static_cast<int>(E), bias, score_fn == 0, groups,
+                                           topk_groups, group_top, topk, renormalize != 0, scale, ids,
+                                           weights, stream));
+}
+
+nv_status nv_kv_quantize(const void* k, const void* v, int64_t k_stride, int64_t v_stride, nv_dtype dt,
+                         int64_t rows, uint8_t* k_codes, float* k_scales, uint8_t* v_codes,
+                         float* v_scales, nv_kv_mode mode, int64_t P, int H, int block, int D,
+                         const int32_t* pages, int64_t max_pages, const int32_t* starts,
+                         const int32_t* lens, int64_t S, uint32_t* flags, nv_stream_t stream) {
+    const nvq::KvCache c{k_codes, k_scales, v_codes, v_scales, P, H, block, D, mode};
+    bool empty = false;
+    nv_status st = check_kv(dt, rows, c, S, max_pages, &empty);
+    if (st != NV_OK || empty) return st;
+    const nvq::KvSteps steps{pages, starts, lens, max_pages, static_cast<int>(S), rows, flags};
+    st = check_kv_pointers(c, steps);
+    if (st != NV_OK) return st;
+    if (!k || !v || !aligned16(k) || !aligned16(v) || !valid_stride(k_stride, int64_t(H) * D, dt) ||
+        !valid_stride(v_stride, int64_t(H) * D, dt))
+        return NV_ERR_INVALID_ARG;
+    return from_cuda(nvq::launch_kv_quantize(k, v, k_stride, v_stride, dt, c, steps, stream));
+}
+
+nv_status nv_kv_dequantize(const uint8_t* k_codes, const float* k_scales, const uint8_t* v_codes,
+                           const float* v_scales, nv_kv_mode mode, int64_t P, int H, int block, int D,
+                           const int32_t* pages, int64_t max_pages, const int32_t* starts,
+                           const int32_t* lens, int64_t S, nv_dtype dt, int64_t rows, void* k, void* v,
+                           uint32_t* flags, nv_stream_t stream) {
+    const nvq::KvCache c{const_cast<uint8_t*>(k_codes), const_cast<float*>(k_scales),
+                         const_cast<uint8_t*>(v_codes), const_cast<float*>(v_scales), P, H, block, D, mode};
+    bool empty = false;
+    nv_status st = check_kv(dt, rows, c, S, max_pages, &empty);
+    if (st != NV_OK || empty) return st;
+    const nvq::KvSteps steps{pages, starts, lens, max_pages, static_cast<int>(S), rows, flags};
+    st = check_kv_pointers(c, steps);
+    if (st != NV_OK) return st;
+    if (!k || !v || !aligned16(k) || !aligned16(v)) return NV_ERR_INVALID_ARG;
+    return from_cuda(nvq::launch_kv_dequantize(k, v, dt, c, steps, stream));
+}
+
+size_t nv_kv_attention_workspace_size(nv_dtype dt, int64_t rows, int Hq, int H, int block, int D,
+                                      int64_t max_pages, int64_t S, int64_t max_q) {
+    (void)dt, (void)rows, (void)Hq, (void)H, (void)block, (void)D, (void)max_pages, (void)S, (void)max_q;
+    return 0;
+}
+
+nv_status nv_kv_attention(const void* q, int64_t q_stride, nv_dtype dt, int64_t rows, int Hq,
+                          const uint8_t* k_codes, const float* k_scales, const uint8_t* v_codes,
+                          const float* v_scales, nv_kv_mode mode, int64_t P, int H, int block, int D,
+                          const int32_t* pages, int64_t max_pages, const int32_t* starts,
+                          const int32_t* lens, int64_t S, float scale, int causal, int window,
+                          int64_t max_q, void* workspace, size_t workspace_bytes, void* out,
+                          uint32_t* flags, nv_stream_t stream) {
+    const nvq::KvCache c{const_cast<uint8_t*>(k_codes), const_cast<float*>(k_scales),
+                         const_cast<uint8_t*>(v_codes), const_cast<float*>(v_scales), P, H, block, D, mode};
+    bool empty = false;
+    nv_status st = check_kv(dt, rows, c, S, max_pages, &empty);
+    if (st != NV_OK) return st;
+    if (Hq < 1 || Hq > 65536 || Hq % H || window < 0 || (window > 0 && !causal) || max_q < 0 ||
+        rows * Hq > 0x7FFFFFFF)
+        return NV_ERR_INVALID_ARG;
+    const size_t need = nv_kv_attention_workspace_size(dt, rows, Hq, H, block, D, max_pages, S, max_q);
+    if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return NV_ERR_WORKSPACE;
+    if (empty) return NV_OK;
+    const nvq::KvSteps steps{pages, starts, lens, max_pages, static_cast<int>(S), rows, flags};
+    st = check_kv_pointers(c, steps);
+    if (st != NV_OK) return st;
+    if (!q || !out || !aligned16(q) || !aligned16(out) || !valid_stride(q_stride, int64_t(Hq) * D, dt))
+        return NV_ERR_INVALID_ARG;
+    const nvq::KvAttn a{q, q_stride, out, dt, Hq, scale, causal != 0, window};
+    return from_cuda(nvq::launch_kv_attn_simple(a, c, steps, stream));
 }
 
 nv_status nv_gather_qmm_flags(const void* workspace, uint32_t* host_flags, nv_stream_t stream) {

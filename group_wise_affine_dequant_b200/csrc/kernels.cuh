@@ -79,4 +79,9 @@ cudaError_t launch_gather_route(const uint32_t* lhs, const uint32_t* rhs, int64_
                                 int64_t x_rows, int sorted, const GatherWorkspace& ws,
                                 cudaStream_t stream, bool want_problems);
 
+// The router: logits [T, E] -> ids and weights [T, topk].
+cudaError_t launch_moe_route(const void* logits, int dt, int64_t T, int E, const float* bias, int softmax,
+                             int groups, int topk_groups, int group_top, int topk, int renormalize,
+                             float scale, uint32_t* ids, float* weights, cudaStream_t stream);
+
 }  // namespace nvq

@@ -28,7 +28,7 @@
  *     between calls is the sticky pipeline error word (nv_pipeline_error) and
  *     the fixed routing array of nv_gather_qmm_noalloc. All work is enqueued
  *     on `stream` (NULL = the legacy default stream), in call order.
- *   - Device pointers must be 16-byte aligned.
+ *   - Device pointers must be 16-byte aligned (entry points say where 4 will do).
  *   - Argument errors are found on the host before anything is launched and
  *     are returned synchronously: NV_ERR_INVALID_ARG (a shape, pointer or
  *     alignment is wrong), NV_ERR_UNSUPPORTED (a valid-looking combination this
@@ -77,6 +77,9 @@ typedef enum nv_dtype {
 #define NV_FLAG_EXPERT_OUT_OF_RANGE 0x1u /* an rhs id >= E: that row's output is zero */
 #define NV_FLAG_NOT_SORTED 0x2u          /* sorted = 1 but rhs ids decrease somewhere */
 #define NV_FLAG_TOKEN_OUT_OF_RANGE 0x4u  /* an lhs id >= x_rows: that row's output is zero */
+/* Device anomaly flags of the key/value cache calls (their `flags` argument). */
+#define NV_FLAG_PAGE_OUT_OF_RANGE 0x8u   /* a needed page id outside [0, P) */
+#define NV_FLAG_BAD_LENGTH 0x10u         /* starts not ascending in [0, rows], or a length that does not fit */
 
 /* Readable text for a status code (static storage, never NULL). */
 const char* nv_status_string(nv_status s);
@@ -316,6 +319,139 @@ nv_status nv_moe_swiglu(const void* x, nv_dtype dt, int64_t T, int64_t K, const 
                         const void* down_scales, const void* down_biases, int group_size,
                         int bits, void* workspace, size_t workspace_bytes, void* y,
                         nv_stream_t stream);
+
+/*
+ * The router in front of the routed experts: from each token's logits to the
+ * expert ids and routing weights that nv_moe_swiglu and nv_gather_qmm take.
+ *
+ * logits  [T, E] in `dt` (NV_F32 or NV_BF16); bias fp32 [E] or NULL.
+ * ids     uint32 [T, topk], weights fp32 [T, topk] (outputs; 4-byte aligned).
+ *   s = softmax(logits) over the experts (score_fn 0) or 1 / (1 + e^-logits)
+ *       (score_fn 1);  c = s + bias.
+ *   groups > 1: the experts form `groups` runs of E / groups; a group's score
+ *       is its largest c (group_top 1) or the sum of its two largest
+ *       (group_top 2); only the topk_groups groups with the largest scores stay
+ *       open. Ties go to the lower group.
+ *   ids: the topk largest c among the open groups' experts, largest first; ties
+ *       go to the lower id. Without a bias experts are compared by their
+ *       logits, which order them as their scores do; scores with a bias, and
+ *       sums of two, are compared exactly where fp32 could not tell them apart
+ *       (in fp64).
+ *   weights: s of the chosen (without the bias), divided by their sum if
+ *       renormalize, times scale.
+ * A logit that is NaN or at or below the lowest bf16 (-3.3895e38), -infinity
+ * included, masks its expert: its score is 0, and it is chosen only (lowest id
+ * first, weight 0) where too few others are open. A token whose experts are
+ * all masked gets ids of the lowest experts and weights 0. +infinity counts as
+ * the largest float.
+ * groups must divide E, 1 <= topk_groups <= groups, 1 <= topk <= 64 and topk
+ * <= topk_groups * (E / groups) (NV_ERR_INVALID_ARG); E <= 1023
+ * (NV_ERR_UNSUPPORTED). logits 16-byte aligned, bias 4-byte. T == 0 is a no-op.
+ */
+nv_status nv_moe_route(const void* logits, nv_dtype dt, int64_t T, int64_t E, const float* bias,
+                       int score_fn, int groups, int topk_groups, int group_top, int topk,
+                       int renormalize, float scale, uint32_t* ids, float* weights,
+                       nv_stream_t stream);
+
+/*
+ * The paged 8-bit key/value cache. Keys and values are kept as one byte a
+ * value with one fp32 scale per block of tokens and head:
+ *   codes   uint8 [P, H, block, D] (NV_KV_INT8: two's complement -127..127;
+ *           NV_KV_E4M3: E4M3 without infinities), scales fp32 [P, H];
+ *           value = code * scale. K and V have a codes and a scales array each.
+ * A page is a block of `block` tokens (16, 32, 64 or 128) of H heads of D
+ * values (a multiple of 16 up to 256).
+ * The step descriptor, shared by the three calls (int32 device arrays):
+ *   lens    [S]: tokens of each sequence, this step's included;
+ *   starts  [S + 1]: ascending; rows starts[s] .. starts[s + 1] - 1 of the step
+ *           are the LAST tokens of sequence s, in order (none is allowed);
+ *   pages   [S, max_pages]: block j of sequence s is page pages[s, j]. Only
+ *           entries that the length reaches are read; a page may be shared by
+ *           sequences that read it, but written by one of them only.
+ * Rows below starts[0] and from starts[S] on belong to no sequence: they are
+ * neither read nor written.
+ * Nothing in these arrays can make a call leave its memory: what is out of
+ * range is skipped and flagged in *flags (device memory, or NULL), which the
+ * calls only OR bits into (NV_FLAG_PAGE_OUT_OF_RANGE, NV_FLAG_BAD_LENGTH);
+ * clearing and reading it is the caller's.
+ * Alignment: 16 bytes for codes and for the step's tensors, 4 for the other
+ * arrays. Errors: NV_ERR_INVALID_ARG (sizes, pointers, alignment, mode),
+ * NV_ERR_UNSUPPORTED (dtype, block or D). rows == 0 or S == 0 is a no-op.
+ */
+typedef enum nv_kv_mode {
+    NV_KV_INT8 = 1,
+    NV_KV_E4M3 = 2
+} nv_kv_mode;
+
+/*
+ * Write a step's keys and values into the cache.
+ * k, v    [rows, H, D] in `dt` (NV_F32 or NV_BF16); a row's heads are dense, rows
+ *         are k_stride and v_stride elements apart (at least H * D, a multiple
+ *         of 16 bytes), as in the output of a fused projection.
+ * A block whose first token is written gets scale = amax / 127 (NV_KV_INT8) or
+ * amax / 448 (NV_KV_E4M3), rounded to fp32, of the block's new values. A block that
+ * holds earlier tokens keeps its scale, or gets this one if it is larger; then
+ * its codes are rounded again to the new scale. A code is the representable
+ * value nearest to the exact x / scale, ties to even. A block of zeros has
+ * scale 0 and codes 0. Infinities do not count for amax and are kept as the
+ * largest code, NaN as 0. Slots behind a sequence's last token are not written.
+ */
+nv_status nv_kv_quantize(const void* k, const void* v, int64_t k_stride, int64_t v_stride, nv_dtype dt,
+                         int64_t rows, uint8_t* k_codes, float* k_scales, uint8_t* v_codes,
+                         float* v_scales, nv_kv_mode mode, int64_t P, int H, int block, int D,
+                         const int32_t* pages, int64_t max_pages, const int32_t* starts,
+                         const int32_t* lens, int64_t S, uint32_t* flags, nv_stream_t stream);
+
+/*
+ * Read the step's rows back: k, v [rows, H, D] dense in `dt` (outputs), the fp32
+ * product code * scale, rounded to nearest if dt is NV_BF16. A row whose page is
+ * out of range, or that lies in front of its sequence, reads as zeros.
+ */
+nv_status nv_kv_dequantize(const uint8_t* k_codes, const float* k_scales, const uint8_t* v_codes,
+                           const float* v_scales, nv_kv_mode mode, int64_t P, int H, int block, int D,
+                           const int32_t* pages, int64_t max_pages, const int32_t* starts,
+                           const int32_t* lens, int64_t S, nv_dtype dt, int64_t rows, void* k, void* v,
+                           uint32_t* flags, nv_stream_t stream);
+
+/*
+ * Bytes of device workspace nv_kv_attention needs (0: none, NULL is allowed).
+ * Depends on the sizes given only.
+ */
+size_t nv_kv_attention_workspace_size(nv_dtype dt, int64_t rows, int Hq, int H, int block, int D,
+                                      int64_t max_pages, int64_t S, int64_t max_q);
+
+/*
+ * Attention of a step's queries over the cache. Query head i reads key/value
+ * head i / (Hq / H); the row of sequence s at place p (its last row is at
+ * lens[s] - 1) sees token j if j < lens[s], and
+ *   causal = 1: j <= p, and j > p - window if window > 0;
+ *   causal = 0: every token (window must be 0), as for an encoder's states.
+ *   out = sum_j softmax_j(scale * q . k_j) v_j, k and v as nv_kv_dequantize gives
+ *   them in fp32.
+ * The step's own keys and values have to be in the cache (nv_kv_quantize
+ * before, on the same stream). A row that sees nothing gives zeros; tokens of
+ * a page out of range are not seen.
+ * q       [rows, Hq, D] in `dt` (NV_F32 or NV_BF16), rows q_stride elements apart
+ *         (as k_stride above); out [rows, Hq, D] dense in `dt`. Hq a multiple of H.
+ *         q must be finite: a row that holds NaN or infinities gives no number
+ *         and changes no other row.
+ * max_q   the largest number of rows of one sequence if known, else 0: a hint
+ *         that chooses kernels, results do not depend on its being right.
+ * workspace 16-byte aligned, nv_kv_attention_workspace_size(...) bytes; its
+ *         contents on entry do not matter; calls that share it must not overlap.
+ * Sums and softmax statistics are fp32. A bf16 call of 64 or 128 values a head runs on
+ * the tensor cores in fp16 (queries, scaled by a power of two, and codes are exact there,
+ * softmax weights are rounded to 11 bits); other calls run in fp32. Routing and the
+ * partition of long sequences follow from the sizes and each sequence's
+ * length, so results are deterministic.
+ */
+nv_status nv_kv_attention(const void* q, int64_t q_stride, nv_dtype dt, int64_t rows, int Hq,
+                          const uint8_t* k_codes, const float* k_scales, const uint8_t* v_codes,
+                          const float* v_scales, nv_kv_mode mode, int64_t P, int H, int block, int D,
+                          const int32_t* pages, int64_t max_pages, const int32_t* starts,
+                          const int32_t* lens, int64_t S, float scale, int causal, int window,
+                          int64_t max_q, void* workspace, size_t workspace_bytes, void* out,
+                          uint32_t* flags, nv_stream_t stream);
 
 /* Copy the anomaly flags of the last nv_gather_qmm (or nv_gather_mm) that used
  * `workspace` into *host_flags (a HOST pointer). Synchronises `stream`. */

@@ -1,0 +1,298 @@
+"""Attention over the paged 8-bit cache (nv_kv_attention) against the 64-bit
+reference, at the lengths, groups, masks and descriptors where it can go wrong."""
+import pytest
+import torch
+
+import group_wise_affine_dequant_b200 as nvq
+from tests import kv_reference as R
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+def _cache(P, H, block, D, mode, seed):
+    """Codes that fill their range roughly normally, scales a few times apart from block to block."""
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(P, H, block, D, generator=g).double() * (R.LARGEST[mode] / 4)
+    scales = (torch.exp(0.5 * torch.randn(P, H, generator=g)) * (4 / R.LARGEST[mode])).float()
+    return R.nearest_codes(x, mode), scales
+
+
+def _run(step, q, caches, mode, **kw):
+    kraw, ks, vraw, vs = caches
+    flags = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = torch.full(q.shape, 9.0, dtype=q.dtype, device="cuda")
+    want_flags = kw.pop("expect_flags", 0)
+    qd = kw.pop("qd", None)
+    got = nvq.nv_kv_attention(q.cuda() if qd is None else qd, kraw.view(R.MODES[mode]).cuda(), ks.cuda(),
+                              vraw.view(R.MODES[mode]).cuda(), vs.cuda(), *step.dev(), out=out, flags=flags, **kw)
+    torch.cuda.synchronize()
+    assert int(flags) == want_flags and nvq.nv_pipeline_error() == 0
+    return got.cpu()
+
+
+def _check(step, H, G, D, mode, dtype, seed, causal=True, window=0, q_scale=1.0, scale=None, max_q=None, caches=None):
+    g = torch.Generator().manual_seed(seed)
+    q = (torch.randn(step.rows, H * G, D, generator=g) * q_scale).to(dtype)
+    if caches is None:
+        caches = (*_cache(step.P, H, step.block, D, mode, seed + 1), *_cache(step.P, H, step.block, D, mode, seed + 2))
+    got = _run(step, q, caches, mode, causal=causal, window=window, scale=scale,
+               max_q=step.max_q if max_q is None else max_q)
+    sc = D ** -0.5 if scale is None else scale
+    out, a, dz = R.attention(q, *caches, step, mode, sc, causal, window)
+    room = R.attention_tolerance(out, a, dz, dtype, D, max(step.lens + [1]))
+    lo, hi = int(step.starts[0]), int(step.starts[-1])
+    err = (got.double() - out).abs()[lo:hi]
+    bad = (~(err <= room[lo:hi])).nonzero()
+    assert len(bad) == 0, (f"{len(bad)} of {err.numel()} off, first {bad[0].tolist()}: got {got[lo:hi][tuple(bad[0])]} want "
+                           f"{out[lo:hi][tuple(bad[0])]} room {room[lo:hi][tuple(bad[0])]}")
+    # rows of no sequence are left as they were
+    assert bool((got[:lo] == 9.0).all()) and bool((got[hi:] == 9.0).all())
+    return got
+
+
+DECODE = [  # lens, block, H, G
+    ([1], 16, 1, 1),
+    ([17, 1, 300], 16, 2, 4),
+    ([63, 64, 65, 128, 129], 64, 2, 8),
+    ([1000, 0, 5], 32, 3, 7),
+    ([2500, 130], 128, 1, 16),
+    ([777], 64, 2, 2),
+]
+
+
+@pytest.mark.parametrize("mode", ["int8", "e4m3"])
+@pytest.mark.parametrize("dtype,D", [(BF16, 128), (BF16, 64), (F32, 64), (BF16, 80)])
+@pytest.mark.parametrize("case", range(len(DECODE)))
+def test_one_token(case, dtype, D, mode):
+    lens, block, H, G = DECODE[case]
+    news = [min(1, n) for n in lens]
+    _check(R.Step(lens, news, block, seed=case, lead=case % 2, behind=case % 3), H, G, D, mode, dtype, 100 + case)
+
+
+STEPS = [  # lens, news, block, H, G, window
+    ([5], [5], 16, 1, 1, 0),
+    ([40, 300, 7], [33, 2, 7], 16, 2, 4, 0),
+    ([130, 0, 64, 260], [130, 0, 1, 70], 64, 2, 3, 0),
+    ([300, 290], [300, 17], 128, 1, 8, 100),
+    ([513], [400], 32, 2, 1, 33),
+    ([257, 130, 129], [256, 129, 128], 64, 1, 5, 1),
+    ([600, 1, 2], [3, 1, 2], 64, 2, 4, 0),
+    ([200, 450], [2, 2], 32, 1, 24, 64),
+]
+
+
+@pytest.mark.parametrize("mode", ["int8", "e4m3"])
+@pytest.mark.parametrize("dtype,D", [(BF16, 128), (BF16, 64), (F32, 128), (BF16, 16)])
+@pytest.mark.parametrize("case", range(len(STEPS)))
+def test_steps_of_many_tokens(case, dtype, D, mode):
+    lens, news, block, H, G, window = STEPS[case]
+    _check(R.Step(lens, news, block, seed=case, lead=case % 3, behind=case % 2), H, G, D, mode, dtype, 200 + case,
+           window=window)
+
+
+@pytest.mark.parametrize("dtype,D", [(BF16, 128), (BF16, 64), (F32, 64)])
+@pytest.mark.parametrize("hint", [0, 1, 5, 10 ** 6])
+def test_the_hint_changes_no_result_beyond_rounding(dtype, D, hint):
+    _check(R.Step([300, 70, 9], [140, 5, 1], 64, seed=1), 2, 4, D, "int8", dtype, 300, max_q=hint)
+
+
+@pytest.mark.parametrize("dtype,D", [(BF16, 128), (BF16, 64), (F32, 64)])
+@pytest.mark.parametrize("news", [[1, 1, 1], [40, 150, 3]])
+def test_every_token_of_another_sequence(dtype, D, news):
+    """causal = 0: queries of any number over an encoder's states, more than there are states among them."""
+    _check(R.Step([100, 149, 3], [min(a, b) for a, b in zip(news, [100, 149, 3])], 32, seed=2), 2, 2, D, "e4m3", dtype, 310,
+           causal=False)
+
+
+@pytest.mark.parametrize("dtype,D", [(BF16, 128), (BF16, 64)])
+@pytest.mark.parametrize("q_scale", [1e-20, 30.0, 3000.0])
+def test_flat_and_peaked_rows(dtype, D, q_scale):
+    """Scores from all alike to one that takes all the weight, tiny and large queries."""
+    step = R.Step([700, 300], [1, 200], 64, seed=3)
+    _check(step, 2, 4, D, "int8", dtype, 320, q_scale=q_scale)
+
+
+@pytest.mark.parametrize("dtype,D,news", [(BF16, 128, 1), (BF16, 128, 300), (BF16, 64, 1), (BF16, 64, 300), (F32, 64, 9)])
+def test_blocks_of_very_different_scales(dtype, D, news):
+    """Value scales from 1e-12 to 1e6 and blocks of zeros, key scales of zero: a block that
+    is large but hardly attended to hides nothing."""
+    H, G, mode = 2, 4, "int8"
+    step = R.Step([640], [news], 64, seed=4)
+    kraw, ks = _cache(step.P, H, 64, D, mode, 1)
+    vraw, vs = _cache(step.P, H, 64, D, mode, 2)
+    ids = step.pages[0, :10].long()
+    vs[ids] = torch.tensor([1e-3, 0.0, 1e-12, 1e6, 1e-3, 1e-8, 0.0, 1e2, 1e-4, 1e-2])[:, None].float()
+    vraw[ids[1]] = 0
+    vraw[ids[6]] = 0
+    ks[ids[2]] = 0
+    # keys against which every query scores far below the rest, where the values are huge
+    kraw[ids[3]] = 0
+    kraw[ids[3], :, :, 0] = 129  # -127
+    g = torch.Generator().manual_seed(7)
+    q = torch.randn(step.rows, H * G, D, generator=g)
+    q[:, :, 0] = 60.0
+    q = q.to(dtype)
+    ks[ids[3]] = 0.05
+    caches = (kraw, ks, vraw, vs)
+    got = _run(step, q, caches, mode, max_q=news)
+    out, a, dz = R.attention(q, *caches, step, mode, D ** -0.5)
+    room = R.attention_tolerance(out, a, dz, dtype, D, 640)
+    err = (got.double() - out).abs()
+    assert bool((err <= room).all()), float((err / room).max())
+
+
+@pytest.mark.parametrize("dtype,D", [(BF16, 128), (BF16, 64), (F32, 64)])
+@pytest.mark.parametrize("news", [1, 100])
+def test_nothing_visible_and_garbage_out_of_sight(dtype, D, news):
+    """Slots behind the last token and unused pages hold NaN codes and NaN scales, table
+    entries behind the length are nonsense: nothing of it is seen."""
+    H, G, mode = 1, 4, "e4m3"
+    step = R.Step([201, 0, 130], [news, 0, min(news, 130)], 64, seed=5)
+    caches = [*_cache(step.P, H, 64, D, mode, 1), *_cache(step.P, H, 64, D, mode, 2)]
+    used = {int(p) for s in range(3) for p in step.pages[s, : -(-step.lens[s] // 64)]}
+    for raw, sc in ((caches[0], caches[1]), (caches[2], caches[3])):
+        for p in range(step.P):
+            if p not in used:
+                raw[p] = 0x7F
+                sc[p] = float("nan")
+        for s in (0, 2):
+            raw[int(step.pages[s, step.lens[s] // 64]), :, step.lens[s] % 64:] = 0x7F
+    _check(step, H, G, D, mode, dtype, 330, caches=tuple(caches))
+    # queries for which nothing is left: a length of zero, or shorter than the step's rows
+    q = torch.randn(50, G, D).to(dtype)
+    short = R.Step([64, 64], [30, 20], 64, seed=6)
+    for lens in ([0, 64], [10, 64], [0, 0]):
+        short.lens_t = torch.tensor(lens, dtype=torch.int32)
+        c = (*_cache(short.P, H, 64, D, mode, 1), *_cache(short.P, H, 64, D, mode, 2))
+        got = _run(short, q, c, mode, max_q=30, expect_flags=R.LENGTH_FLAG)
+        assert bool((got[: 30 - lens[0]] == 0).all()) and bool(torch.isfinite(got.float()).all())
+        if lens[0]:
+            assert bool((got[30 - lens[0]: 30].abs().sum((1, 2)) > 0).all())
+        assert bool((got[30:].abs().sum((1, 2)) > 0).all()) == (lens[1] == 64)
+
+
+@pytest.mark.parametrize("dtype,D", [(BF16, 128), (BF16, 64), (F32, 64)])
+@pytest.mark.parametrize("news", [1, 90])
+def test_pages_out_of_range_are_not_seen(dtype, D, news):
+    H, G, mode = 2, 2, "int8"
+    step = R.Step([200, 100], [news, 1], 32, seed=7)
+    caches = (*_cache(step.P, H, 32, D, mode, 1), *_cache(step.P, H, 32, D, mode, 2))
+    good = step.pages.clone()
+    q = torch.randn(step.rows, H * G, D, generator=torch.Generator().manual_seed(1)).to(dtype)
+    for bad in (-1, step.P, 2 ** 31 - 1):
+        step.pages = good.clone()
+        step.pages[0, 2] = bad
+        got = _run(step, q, caches, mode, max_q=news, expect_flags=R.PAGE_FLAG)
+        step.pages = good
+        out, a, dz = R.attention(q, *caches, step, mode, D ** -0.5, drop=lambda s, j: s == 0 and j // 32 == 2)
+        room = R.attention_tolerance(out, a, dz, dtype, D, 200)
+        assert bool(((got.double() - out).abs() <= room).all())
+    for starts in ([0, 70, 60], [-3, 40, 60], [50, 10, 60], [0, 2 ** 31 - 1, -2 ** 31]):
+        other = R.Step([200, 100], [news, 1], 32, seed=7)
+        other.starts = torch.tensor(starts, dtype=torch.int32)
+        _run(other, q, caches, mode, max_q=0, expect_flags=R.LENGTH_FLAG)
+
+
+@pytest.mark.parametrize("dtype,D,news", [(BF16, 128, 1), (BF16, 128, 140), (BF16, 64, 140), (F32, 64, 3)])
+def test_a_row_that_is_not_finite_stays_alone(dtype, D, news):
+    H, G, mode = 1, 4, "int8"
+    step = R.Step([300, 200], [news, 1], 64, seed=8)
+    caches = (*_cache(step.P, H, 64, D, mode, 1), *_cache(step.P, H, 64, D, mode, 2))
+    q = torch.randn(step.rows, G, D, generator=torch.Generator().manual_seed(1)).to(dtype)
+    clean = _run(step, q, caches, mode, max_q=news)
+    q[0, 1, 5] = float("nan")
+    q[0, 2, 6] = float("inf")
+    got = _run(step, q, caches, mode, max_q=news)
+    assert not bool(torch.isfinite(got[0, 1].float()).any())
+    keep = torch.ones(step.rows, G, dtype=torch.bool)
+    keep[0, 1] = keep[0, 2] = False
+    assert torch.equal(got[keep], clean[keep])
+
+
+@pytest.mark.parametrize("news", [1, 200])
+def test_deterministic_strided_and_on_a_side_stream(news):
+    H, G, D, mode = 2, 4, 128, "int8"
+    step = R.Step([3000, 500], [news, min(news, 70)], 64, seed=9)
+    caches = (*_cache(step.P, H, 64, D, mode, 1), *_cache(step.P, H, 64, D, mode, 2))
+    wide = torch.randn(step.rows, H * G + 2 * H, D, generator=torch.Generator().manual_seed(1)).to(BF16)
+    q = wide[:, : H * G]
+    first = _run(step, q.contiguous(), caches, mode, max_q=news)
+    assert torch.equal(_run(step, q, caches, mode, max_q=news, qd=wide.cuda()[:, : H * G]), first)
+    need = nvq.nv_kv_attention_workspace_size(step.rows, H * G, H, 64, D, step.pages.shape[1], 2, news)
+    ws = torch.full((need + 16,), 255, dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    dev = [t.cuda() for t in (q.contiguous(), caches[0].view(torch.int8), caches[1], caches[2].view(torch.int8), caches[3], *step.dev())]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = nvq.nv_kv_attention(*dev, max_q=news, workspace=ws, stream=side)
+        side.synchronize()
+        assert torch.equal(got.cpu(), first)
+    assert bool((ws[need:] == 255).all())
+
+
+@pytest.mark.parametrize("news", [1, 150])
+def test_capture_and_replay_with_new_lengths(news):
+    H, G, D, mode = 2, 4, 128, "e4m3"
+    step = R.Step([1500, 900], [news, 1], 64, seed=10)
+    caches = (*_cache(step.P, H, 64, D, mode, 1), *_cache(step.P, H, 64, D, mode, 2))
+    q = torch.randn(step.rows, H * G, D, generator=torch.Generator().manual_seed(1)).to(BF16)
+    dev = [q.cuda(), caches[0].view(R.MODES[mode]).cuda(), caches[1].cuda(), caches[2].view(R.MODES[mode]).cuda(),
+           caches[3].cuda(), *step.dev()]
+    nvq.nv_kv_attention(*dev, max_q=news)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = nvq.nv_kv_attention(*dev, max_q=news)
+    for lens in ([1500, 900], [news, 1], [700, 64], [1111, 899]):
+        dev[7].copy_(torch.tensor(lens, dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        step.lens = lens
+        want, a, dz = R.attention(q, *caches, step, mode, D ** -0.5)
+        room = R.attention_tolerance(want, a, dz, BF16, D, 1500)
+        assert bool(((out.cpu().double() - want).abs() <= room).all()), lens
+    assert nvq.nv_pipeline_error() == 0
+    del graph
+
+
+@pytest.mark.parametrize("news,D", [(1, 128), (60, 128), (1, 64), (60, 64)])
+def test_offsets_past_32_bits(news, D):
+    """Pages at the far end of a pool of more than 2^32 bytes of codes (K and V the same array)."""
+    H, G, block = 8, 4, 128
+    P = (1 << 32) // (H * D * block) + 40
+    codes = torch.zeros(P, H, block, D, dtype=torch.int8, device="cuda")
+    scales = torch.zeros(P, H, device="cuda")
+    step = R.Step([300], [news], block)
+    raw, sc = _cache(3, H, block, D, "int8", 3)
+    small = R.Step([300], [news], block)
+    small.pages = torch.tensor([[0, 1, 2]], dtype=torch.int32)
+    step.pages = torch.tensor([[P - 1, P - 3, P - 8]], dtype=torch.int32)
+    codes[step.pages[0].long().cuda()] = raw.view(torch.int8).cuda()
+    scales[step.pages[0].long().cuda()] = sc.cuda()
+    q = torch.randn(news, H * G, D, generator=torch.Generator().manual_seed(1)).to(BF16)
+    got = nvq.nv_kv_attention(q.cuda(), codes, scales, codes, scales, *step.dev(), max_q=news).cpu()
+    out, a, dz = R.attention(q, raw, sc, raw, sc, small, "int8", D ** -0.5)
+    assert bool(((got.double() - out).abs() <= R.attention_tolerance(out, a, dz, BF16, D, 300)).all())
+
+
+def test_refusals():
+    step = R.Step([4], [4], 16)
+    q = torch.zeros(4, 4, 64, dtype=BF16, device="cuda")
+    kc = torch.zeros(step.P, 2, 16, 64, dtype=torch.int8, device="cuda")
+    ks = torch.zeros(step.P, 2, device="cuda")
+    d = step.dev()
+    assert nvq.nv_kv_attention(q, kc, ks, kc, ks, *d).shape == (4, 4, 64)
+    for bad in (dict(q=q.half()), dict(q=q[:, :3]), dict(window=-1), dict(window=4, causal=False), dict(max_q=-1)):
+        a = dict(q=q, causal=True, window=0, max_q=0)
+        a.update(bad)
+        with pytest.raises(nvq.NvqError):
+            nvq.nv_kv_attention(a["q"], kc, ks, kc, ks, *d, causal=a["causal"], window=a["window"], max_q=a["max_q"])
+    for bad in (dict(q=q[:, :, :32]), dict(q=q.cpu()), dict(q=q[0]), dict(out=q.float()), dict(kc=kc.float())):
+        a = dict(q=q, out=None, kc=kc)
+        a.update(bad)
+        with pytest.raises(ValueError):
+            nvq.nv_kv_attention(a["q"], a["kc"], ks, a["kc"], ks, *d, out=a["out"])
+    assert nvq.nv_kv_attention(q[:0], kc, ks, kc, ks, *d).shape == (0, 4, 64)
