@@ -50,7 +50,7 @@ nv_status check_kv(nv_dtype dt, int64_t rows, const nvq::KvCache& c, int64_t S, 
     if (c.mode != NV_KV_INT8 && c.mode != NV_KV_E4M3) return NV_ERR_INVALID_ARG;
     if (rows < 0 || rows > 0x7FFFFFFF || S < 0 || S > 0xFFFFFF || max_pages < 0 ||
         max_pages > 0x7FFFFFFF || c.P < 0 || c.P > 0x7FFFFFFF || c.H < 1 || c.H > 1024 || c.D < 1 ||
-        c.block < 1)
+        c.block < 1 || c.P * c.H > 0x7FFFFFFF)
         return NV_ERR_INVALID_ARG;
     if (c.D % 16 || c.D > 256 || (c.block != 16 && c.block != 32 && c.block != 64 && c.block != 128))
         return NV_ERR_UNSUPPORTED;
@@ -66,6 +66,12 @@ nv_status check_kv_pointers(const nvq::KvCache& c, const nvq::KvSteps& st) {
                           static_cast<const void*>(st.lens), static_cast<const void*>(st.flags)})
         if (!aligned4(p)) return NV_ERR_INVALID_ARG;
     return NV_OK;
+}
+// Which attention kernels a call takes: a pure function of the sizes.
+enum class KvRoute { kSimple, kDecode };
+KvRoute kv_attn_route(nv_dtype dt, int D, int64_t P, int64_t max_q, int64_t G) {
+    if (dt != NV_BF16 || (D != 64 && D != 128) || P == 0) return KvRoute::kSimple;
+    return max_q > 0 && max_q * G <= 16 ? KvRoute::kDecode : KvRoute::kSimple;
 }
 // A row stride in elements: the heads fit and every row starts on 16 bytes.
 bool valid_stride(int64_t stride, int64_t least, nv_dtype dt) {
@@ -375,8 +381,11 @@ nv_status nv_kv_dequantize(const uint8_t* k_codes, const float* k_scales, const 
 
 size_t nv_kv_attention_workspace_size(nv_dtype dt, int64_t rows, int Hq, int H, int block, int D,
                                       int64_t max_pages, int64_t S, int64_t max_q) {
-    (void)dt, (void)rows, (void)Hq, (void)H, (void)block, (void)D, (void)max_pages, (void)S, (void)max_q;
-    return 0;
+    if (rows <= 0 || S <= 0 || max_pages < 0 || Hq < 1 || H < 1 || Hq % H || block < 1 || D < 1 || max_q < 0 ||
+        rows > 0x7FFFFFFF || S > 0xFFFFFF || max_pages > 0x7FFFFFFF)
+        return 0;
+    if (kv_attn_route(dt, D, 1, max_q, Hq / H) != KvRoute::kDecode) return 0;
+    return nvq::kv_decode_plan({rows, S, max_pages, Hq, H, block, D, true}, sm_count()).bytes(D);
 }
 
 nv_status nv_kv_attention(const void* q, int64_t q_stride, nv_dtype dt, int64_t rows, int Hq,
@@ -403,6 +412,11 @@ nv_status nv_kv_attention(const void* q, int64_t q_stride, nv_dtype dt, int64_t 
     if (!q || !out || !aligned16(q) || !aligned16(out) || !valid_stride(q_stride, int64_t(Hq) * D, dt))
         return NV_ERR_INVALID_ARG;
     const nvq::KvAttn a{q, q_stride, out, dt, Hq, scale, causal != 0, window};
+    if (kv_attn_route(dt, D, P, max_q, Hq / H) == KvRoute::kDecode) {
+        const int sms = sm_count();
+        const nvq::KvDecodePlan plan = nvq::kv_decode_plan({rows, S, max_pages, Hq, H, block, D, true}, sms);
+        return from_cuda(nvq::launch_kv_attn_decode(a, c, steps, plan, workspace, stream, sms));
+    }
     return from_cuda(nvq::launch_kv_attn_simple(a, c, steps, stream));
 }
 
@@ -428,10 +442,11 @@ nv_status nv_pipeline_error(uint32_t* host_code) {
     const unsigned int d = nvq::tc_gather_mm_error_take();
     const unsigned int g = nvq::tc_gather_t0_error_take();
     const unsigned int t = nvq::selftest_error_take();
+    const unsigned int kd = nvq::kv_attn_decode_error_take();
     if (a == 0xFFFFFFFFu || b == 0xFFFFFFFFu || c == 0xFFFFFFFFu || d == 0xFFFFFFFFu ||
-        g == 0xFFFFFFFFu || t == 0xFFFFFFFFu)
+        g == 0xFFFFFFFFu || t == 0xFFFFFFFFu || kd == 0xFFFFFFFFu)
         return NV_ERR_CUDA;
-    *host_code = a ? a : b ? b : c ? c : d ? d : g ? g : t;
+    *host_code = a ? a : b ? b : c ? c : d ? d : g ? g : kd ? kd : t;
     return NV_OK;
 }
 

@@ -128,4 +128,24 @@ struct KvAttn {
 // Plain kernel: any head size, fp32 or bf16, one CTA per (row, query head).
 cudaError_t launch_kv_attn_simple(const KvAttn& a, const KvCache& c, const KvSteps& st, cudaStream_t stream);
 
+// Kernel for few rows a sequence (bf16, D 64 or 128): sequences are cut into
+// chunks that a second kernel joins. `only`: every sequence is its; else it takes those of at
+// most 16 flattened rows (token, head of the group) and leaves the others.
+struct KvDecodeSizes {
+    int64_t rows, S, max_pages;
+    int Hq, H, block, D;
+    bool only;
+};
+struct KvDecodePlan {
+    int target, max_chunks, row_limit;
+    int64_t part_rows;
+    size_t bytes(int D) const {
+        return max_chunks > 1 ? static_cast<size_t>(part_rows) * max_chunks * (D + 1) * sizeof(float) : 0;
+    }
+};
+KvDecodePlan kv_decode_plan(const KvDecodeSizes& z, int num_sms);
+cudaError_t launch_kv_attn_decode(const KvAttn& a, const KvCache& c, const KvSteps& st, const KvDecodePlan& plan,
+                                  void* workspace, cudaStream_t stream, int num_sms);
+unsigned int kv_attn_decode_error_take();
+
 }  // namespace nvq

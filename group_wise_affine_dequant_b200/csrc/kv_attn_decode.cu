@@ -1,0 +1,665 @@
+// Attention over the paged 8-bit cache for few query rows a sequence (bf16, 64 or
+// 128 values a head): the work is reading the cache once.
+//
+// A row tile is 16 query rows of one sequence and key/value head, row =
+// (token, query head of the group); an item is a row tile against a chunk of
+// the sequence (a multiple of 64 tokens). Items of all sequences are counted
+// by every CTA from the lengths (a prefix sum in shared memory), so the grid is
+// one wave of resident CTAs and the host needs to know no length.
+//
+// Per CTA: a producer warp fetches page ids and scales of the next item and
+// streams its codes by TMA, 64 tokens of K and V a stage (boxes of
+// min(block, 64) tokens, swizzled so that all fragment reads but the 64-wide
+// values' are free of bank conflicts). Four consumer warps take 16 of the 64
+// tokens each, with their own running maximum, sum and output: scores by mma.m16n8k16
+// (fp16 codes are exact), weights straight from the score fragments into the second
+// product's A operand, values transposed byte-wise in registers. No barrier
+// between the warps inside an item; they join at its end. Items of a sequence that
+// takes several write (output, log-sum) to the workspace and a second kernel
+// joins them in chunk order, so results do not depend on timing.
+//
+// Bound: the code bytes, 2 * D a token and key/value head.
+#include <cstdint>
+
+#include "kv_mma.cuh"
+
+namespace nvq {
+namespace {
+
+constexpr int kTile = 64;        // tokens a stage
+constexpr int kConsumers = 4;    // warps
+constexpr int kThreads = 32 * (kConsumers + 1);
+constexpr int kChunkMax = 1024;  // tokens an item: long enough that joining costs under 2 %
+constexpr int kChunkMin = 128;
+constexpr int kBlocksMax = kChunkMax / 16 + 1;
+
+template <int D>
+constexpr int kStages = D == 128 ? 4 : 8;
+
+struct ItemMeta {
+    int64_t row0;       // first row of the sequence in the step
+    int64_t part;       // partial index of (row 0 of the tile, chunk 0), or -1: the item writes the output
+    int h, s;
+    int f0, rows;       // the tile's first flattened row (token * G + group head) and its rows
+    int first;          // place of the sequence's first row
+    int len;
+    int t0, t1;         // tokens [t0, t1) of the chunk; t0 a multiple of 64
+    int lo_max, hi_min; // tokens in [lo_max, hi_min) are visible to every row of the tile
+    int chunk, pstride; // partial index of row r: part + r * pstride (+ chunk)
+    int block0;         // t0 / block
+    float vmax;         // largest value scale of the item
+};
+
+// Chunk length for a span of tokens: `target` chunks a sequence where the GPU would be
+// short of work, but never so long that one sequence is the tail of the grid.
+__host__ __device__ inline int chunk_tokens(int64_t span, int target) {
+    int64_t c = (span + target - 1) / target;
+    c = (c + kTile - 1) / kTile * kTile;
+    return static_cast<int>(c < kChunkMin ? kChunkMin : c > kChunkMax ? kChunkMax : c);
+}
+
+struct DecodeArgs {
+    KvAttn a;
+    KvCache c;
+    KvSteps st;
+    int target;      // chunks a sequence is cut into (see chunk_tokens)
+    int max_chunks;  // partials a row has room for
+    int row_limit;   // sequences of more flattened rows are not this kernel's (0: all are)
+    float* part_o;   // [rows][max_chunks][D]
+    float* part_lse; // [rows][max_chunks]
+};
+
+// Where a sequence's items come from.
+struct SeqWork {
+    SeqSpan span;
+    int lo;      // first token any row sees, rounded down to 64
+    int chunk, chunks, tiles;
+};
+__device__ __forceinline__ SeqWork seq_work(const DecodeArgs& p, int s) {
+    SeqWork w;
+    w.span = seq_span(p.st, s, p.c.block);
+    const int G = p.a.Hq / p.c.H;
+    const int64_t rows = static_cast<int64_t>(w.span.n) * G;
+    w.lo = 0;
+    if (p.a.window > 0 && w.span.first + 1 > p.a.window) w.lo = (w.span.first + 1 - p.a.window) / kTile * kTile;
+    const int span = w.span.len - w.lo;
+    w.chunk = chunk_tokens(span > 0 ? span : 1, p.target);
+    w.chunks = span > 0 ? (span + w.chunk - 1) / w.chunk : 1;  // a row that sees nothing still writes zeros
+    w.tiles = static_cast<int>((rows + 15) / 16);
+    if (p.row_limit > 0 && rows > p.row_limit) w.tiles = 0;
+    return w;
+}
+// Partial index of flattened row f of sequence s and head h, chunk 0.
+__device__ __forceinline__ int64_t part_row(const DecodeArgs& p, const SeqSpan& span, int s, int h, int f) {
+    const int G = p.a.Hq / p.c.H;
+    if (p.row_limit > 0) return (static_cast<int64_t>(s) * p.c.H + h) * p.row_limit + f;
+    return (span.row0 + f / G) * p.a.Hq + h * G + f % G;
+}
+
+template <int MODE, int D>
+__global__ void __launch_bounds__(kThreads, 2)
+kv_attn_decode_kernel(const __grid_constant__ DecodeArgs p, const __grid_constant__ CUtensorMap kmap,
+                      const __grid_constant__ CUtensorMap vmap) {
+    constexpr int NS = kStages<D>;
+    constexpr int kHalf = kTile * D;  // bytes of K (or V) a stage
+    constexpr int KS = D / 16;        // k-steps of the first product
+    constexpr int NT = D / 8;         // n-tiles of the second
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    uint8_t* stages = smem;                                            // [NS][2][kHalf]
+    float* join = reinterpret_cast<float*>(smem + NS * 2 * kHalf);     // [4][16][D]
+    __shared__ __align__(8) uint64_t full[NS], empty[NS], meta_full[2], meta_empty[2];
+    __shared__ ItemMeta meta[2];
+    __shared__ BlockScales scales[2][kBlocksMax];
+    __shared__ int64_t prefix[kThreads + 1];
+    __shared__ float join_m[kConsumers][16], join_l[kConsumers][16];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+    if (tid == 0) {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], kConsumers);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&meta_full[i], 1);
+            mbar_init(&meta_empty[i], kConsumers);
+        }
+        mbar_init_fence();
+    }
+    pdl_launch_dependents();
+    pdl_wait();
+
+    // items before each thread's run of sequences
+    const int G = p.a.Hq / p.c.H;
+    const int per = (p.st.S + kThreads - 1) / kThreads;
+    {
+        int64_t mine = 0;
+        for (int i = 0; i < per; ++i) {
+            const int s = tid * per + i;
+            if (s >= p.st.S) break;
+            const SeqWork w = seq_work(p, s);
+            mine += static_cast<int64_t>(w.tiles) * w.chunks;
+        }
+        prefix[tid + 1] = mine;
+        if (tid == 0) prefix[0] = 0;
+        __syncthreads();
+        if (warp == 0) {  // five values a lane
+            int64_t v[kThreads / 32], sum = 0;
+#pragma unroll
+            for (int i = 0; i < kThreads / 32; ++i) {
+                sum += prefix[lane * (kThreads / 32) + i + 1];
+                v[i] = sum;
+            }
+            int64_t before = sum;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t n = __shfl_up_sync(0xffffffffu, before, o);
+                if (lane >= o) before += n;
+            }
+            before -= sum;
+#pragma unroll
+            for (int i = 0; i < kThreads / 32; ++i) prefix[lane * (kThreads / 32) + i + 1] = before + v[i];
+        }
+        __syncthreads();
+    }
+    const int64_t total = prefix[kThreads] * p.c.H;
+    bool ok = true;
+
+    if (warp == kConsumers) {
+        // ------------------------------------------------------------ producer
+        int stage = 0;
+        uint32_t phase = 0;
+        int it = 0;
+        const int box = p.c.block < kTile ? p.c.block : kTile;
+        for (int64_t w = blockIdx.x; ok && w < total; w += gridDim.x, ++it) {
+            const int slot = it & 1;
+            ok = mbar_wait(&meta_empty[slot], ((it >> 1) & 1) ^ 1, 0x61);
+            if (!ok) break;
+            // the sequence: its thread's run, then the sequence in the run
+            const int64_t u = w / p.c.H;
+            const int h = static_cast<int>(w - u * p.c.H);
+            int lo = 0, hi = kThreads;
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) / 2;
+                if (prefix[mid] <= u) lo = mid; else hi = mid;
+            }
+            int64_t left = u - prefix[lo];
+            int s = lo * per;
+            SeqWork sw = seq_work(p, s);
+            while (left >= static_cast<int64_t>(sw.tiles) * sw.chunks) {
+                left -= static_cast<int64_t>(sw.tiles) * sw.chunks;
+                sw = seq_work(p, ++s);
+            }
+            const int tile = static_cast<int>(left / sw.chunks), chunk = static_cast<int>(left - static_cast<int64_t>(tile) * sw.chunks);
+            const int f0 = tile * 16;
+            const int64_t seq_rows = static_cast<int64_t>(sw.span.n) * G;
+            const int rows = seq_rows - f0 < 16 ? static_cast<int>(seq_rows - f0) : 16;
+            const int p0 = sw.span.first + f0 / G, p1 = sw.span.first + (f0 + rows - 1) / G;  // places of its first and last row
+            int t0 = sw.lo + chunk * sw.chunk;
+            int t1 = t0 + sw.chunk < sw.span.len ? t0 + sw.chunk : sw.span.len;
+            int lo_max = 0, hi_min = sw.span.len, lo_min = 0, hi_max = sw.span.len;
+            if (p.a.causal) {
+                hi_min = p0 + 1 < hi_min ? p0 + 1 : hi_min;
+                hi_max = p1 + 1 < hi_max ? p1 + 1 : hi_max;
+                if (p.a.window > 0) {
+                    lo_max = p1 + 1 > p.a.window ? p1 + 1 - p.a.window : 0;
+                    lo_min = p0 + 1 > p.a.window ? p0 + 1 - p.a.window : 0;
+                }
+            }
+            if (t1 > hi_max) t1 = hi_max;
+            if (t0 < lo_min / kTile * kTile) t0 = lo_min / kTile * kTile;
+            if (t1 < t0) t1 = t0;
+            const int block0 = t0 / p.c.block;
+            const int blocks = t1 > t0 ? (t1 - 1) / p.c.block - block0 + 1 : 0;
+            float vmax = 0.f;
+            float vs_of[(kBlocksMax + 31) / 32];
+#pragma unroll
+            for (int i = 0; i < (kBlocksMax + 31) / 32; ++i) {
+                const int b = lane + 32 * i;
+                vs_of[i] = 0.f;
+                if (b < blocks) {
+                    const int page = page_of(p.st, p.c, s, block0 + b);
+                    float ks = -1.f;
+                    if (page >= 0) {
+                        const int64_t ph = static_cast<int64_t>(page) * p.c.H + h;
+                        ks = __ldg(p.c.k_scales + ph);
+                        vs_of[i] = __ldg(p.c.v_scales + ph);
+                    }
+                    scales[slot][b].ks = ks;
+                    scales[slot][b].page = page;
+                    vmax = fmaxf(vmax, vs_of[i]);
+                }
+            }
+#pragma unroll
+            for (int o = 16; o; o >>= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, o));
+#pragma unroll
+            for (int i = 0; i < (kBlocksMax + 31) / 32; ++i) {
+                const int b = lane + 32 * i;
+                if (b < blocks) {
+                    const float lg = vs_of[i] > 0.f ? fmaxf(log2f(vs_of[i]) - log2f(vmax), -100.f) : 0.f;
+                    scales[slot][b].lg = lg;
+                    scales[slot][b].inv = exp2f(-lg);
+                }
+            }
+            if (lane == 0) {
+                ItemMeta& m = meta[slot];
+                m.row0 = sw.span.row0;
+                m.part = sw.chunks > 1 ? part_row(p, sw.span, s, h, f0) : -1;
+                m.h = h;
+                m.s = s;
+                m.f0 = f0;
+                m.rows = rows;
+                m.first = sw.span.first;
+                m.len = sw.span.len;
+                m.t0 = t0;
+                m.t1 = t1;
+                m.lo_max = lo_max;
+                m.hi_min = hi_min;
+                m.chunk = chunk;
+                m.block0 = block0;
+                m.vmax = vmax;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&meta_full[slot]);
+            for (int t = t0; ok && t < t1; t += kTile) {
+                ok = mbar_wait(&empty[stage], phase ^ 1, 0x62);
+                if (!ok) break;
+                if (lane == 0) {
+                    uint8_t* k = stages + stage * 2 * kHalf;
+                    uint8_t* v = k + kHalf;
+                    int boxes = 0;
+                    for (int j = t; j < t + kTile && j < t1; j += box)
+                        boxes += scales[slot][j / p.c.block - block0].page >= 0;
+                    mbar_expect_tx(&full[stage], static_cast<uint32_t>(2 * boxes * box * D));
+                    for (int j = t; j < t + kTile && j < t1; j += box) {
+                        const int page = scales[slot][j / p.c.block - block0].page;
+                        if (page < 0) continue;
+                        const int ph = page * p.c.H + h;
+                        tma_load_3d(k + (j - t) * D, &kmap, &full[stage], 0, j % p.c.block, ph);
+                        tma_load_3d(v + (j - t) * D, &vmap, &full[stage], 0, j % p.c.block, ph);
+                    }
+                }
+                __syncwarp();
+                if (++stage == NS) { stage = 0; phase ^= 1; }
+            }
+        }
+        if (!ok)  // a wait gave up: let the copies in flight land before the CTA ends
+            for (int i = 0; i < NS; ++i) mbar_wait(&full[i], phase ^ (i >= stage), 0x63, 10000000);
+    } else {
+        // ----------------------------------------------------------- consumers
+        const int g = lane >> 2, t4 = lane & 3;
+        int stage = 0;
+        uint32_t phase = 0;
+        int it = 0;
+        for (int64_t w = blockIdx.x; ok && w < total; w += gridDim.x, ++it) {
+            const int slot = it & 1;
+            ok = mbar_wait(&meta_full[slot], (it >> 1) & 1, 0x64);
+            if (!ok) break;
+            const ItemMeta& m = meta[slot];
+            // this lane's two rows (g, g + 8): queries, scale, visible range
+            uint32_t qa[KS][4];
+            float zc[2];
+            int row_lo[2], row_hi[2];
+            bool bad[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int row = g + 8 * r;
+                row_lo[r] = 0;
+                row_hi[r] = m.len;
+                bad[r] = false;
+                uint4 raw[D / 32];
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) raw[i] = make_uint4(0, 0, 0, 0);
+                if (row < m.rows) {
+                    const int f = m.f0 + row, tok = f / G;
+                    const int pos = m.first + tok;
+                    if (p.a.causal) {
+                        row_hi[r] = pos + 1 < m.len ? pos + 1 : m.len;
+                        if (p.a.window > 0 && pos + 1 > p.a.window) row_lo[r] = pos + 1 - p.a.window;
+                    }
+                    const uint4* q = reinterpret_cast<const uint4*>(
+                        static_cast<const uint16_t*>(p.a.q) + (m.row0 + tok) * p.a.q_stride +
+                        (static_cast<int64_t>(m.h) * G + f % G) * D + t4 * (D / 4));
+#pragma unroll
+                    for (int i = 0; i < D / 32; ++i) raw[i] = __ldg(q + i);
+                }
+                uint32_t most = 0;
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    const uint32_t u[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) most = max(most, max((u[j] << 16) & 0x7FFFFFFFu, u[j] & 0x7FFF0000u));
+                }
+                most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
+                most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
+                bad[r] = most >= 0x7F800000u;
+                const uint32_t ex = row_exponent(most);
+                const float down = pow2_bits(254u - ex);
+                zc[r] = p.a.scale * kLog2e * pow2_bits(ex);
+                // word i, 16-bit pairs: values 8 i + {0, 1}, {2, 3} are k-step 2 i's b0 and b1 pairs, and so on
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    const uint32_t u[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t h2 = f2_to_h2(__uint_as_float(u[j] << 16) * down,
+                                                     __uint_as_float(u[j] & 0xFFFF0000u) * down);
+                        qa[2 * i + j / 2][r + 2 * (j & 1)] = h2;
+                    }
+                }
+            }
+            float o[NT][4];
+#pragma unroll
+            for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+            float ref[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+
+            for (int t = m.t0; ok && t < m.t1; t += kTile) {
+                ok = mbar_wait(&full[stage], phase, 0x65);
+                if (!ok) break;
+                const int j0 = t + 16 * warp;
+                const BlockScales bs = scales[slot][j0 < m.t1 ? j0 / p.c.block - m.block0 : 0];
+                if (j0 < m.t1 && bs.ks >= 0.f) {  // else nothing of these 16 tokens is seen
+                    const uint8_t* kt = stages + stage * 2 * kHalf + 16 * warp * D;
+                    const uint8_t* vt = kt + kHalf;
+                    float c[2][4];
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.f;
+                        const int row = 8 * n + g;
+#pragma unroll
+                        for (int i = 0; i < D / 64; ++i) {
+                            uint4 u;
+                            if constexpr (D == 128)
+                                u = *reinterpret_cast<const uint4*>(kt + row * 128 + ((2 * t4 + i) ^ (row & 7)) * 16);
+                            else
+                                u = *reinterpret_cast<const uint4*>(kt + row * 64 + (t4 ^ ((row >> 1) & 3)) * 16);
+                            const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const uint32_t y = prepare_word<MODE>(x[j]);
+                                const int ks = 4 * i + j;
+                                mma_f16_16816(c[n], qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3], pair_lo_h2<MODE>(y),
+                                              pair_hi_h2<MODE>(y));
+                            }
+                        }
+                    }
+                    const bool whole = j0 >= m.lo_max && j0 + 16 <= m.hi_min;
+                    float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int r = e >> 1, j = j0 + 8 * n + 2 * t4 + (e & 1);
+                            float z = c[n][e] * (zc[r] * bs.ks);
+                            if (!whole && (j < row_lo[r] || j >= row_hi[r])) z = -INFINITY;
+                            c[n][e] = z;
+                            mx[r] = fmaxf(mx[r], z);
+                        }
+                    bool grow = false;
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+                        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2)) + bs.lg;
+                        grow |= mx[r] > ref[r] + kSlack;
+                    }
+                    if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            // each row by itself: its result must not depend on its neighbours
+                            const bool up = mx[r] > ref[r] + kSlack;
+                            const float f = up ? exp2f(ref[r] - mx[r]) : 1.f;
+                            ref[r] = up ? mx[r] : ref[r];
+                            l[r] *= f;
+#pragma unroll
+                            for (int i = 0; i < NT; ++i) {
+                                o[i][2 * r] *= f;
+                                o[i][2 * r + 1] *= f;
+                            }
+                        }
+                    }
+                    uint32_t pa[4];
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const float base = bs.lg + kLift - (ref[r] > -INFINITY ? ref[r] : 0.f);
+                        float sum = 0.f;
+#pragma unroll
+                        for (int n = 0; n < 2; ++n) {
+                            const float w0 = exp2_approx(c[n][2 * r] + base), w1 = exp2_approx(c[n][2 * r + 1] + base);
+                            sum += w0 + w1;
+                            pa[2 * n + r] = f2_to_h2(w0, w1);
+                        }
+                        l[r] = fmaf(sum, bs.inv, l[r]);
+                    }
+                    // values: tokens 2 t4, 2 t4 + 1 (b0) and 8 + 2 t4, 9 + 2 t4 (b1); n-tile i, column g is value
+                    // (D / 8) g + i
+                    uint32_t v[4][D / 32];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int row = 8 * (q >> 1) + 2 * t4 + (q & 1);
+                        if constexpr (D == 128) {
+                            const uint4 u = *reinterpret_cast<const uint4*>(vt + row * 128 + (g ^ (row & 7)) * 16);
+                            v[q][0] = u.x; v[q][1] = u.y; v[q][2] = u.z; v[q][3] = u.w;
+                        } else {
+                            const uint2 u = *reinterpret_cast<const uint2*>(
+                                vt + row * 64 + ((g >> 1) ^ ((row >> 1) & 3)) * 16 + (g & 1) * 8);
+                            v[q][0] = u.x; v[q][1] = u.y;
+                        }
+                        // a slot behind the last token may hold a NaN code
+                        if (MODE == NV_KV_E4M3 && !whole && j0 + row >= m.len)
+#pragma unroll
+                            for (int i = 0; i < D / 32; ++i) v[q][i] = 0;
+                    }
+#pragma unroll
+                    for (int i = 0; i < D / 32; ++i) {
+                        const uint32_t a0 = prepare_word<MODE>(v[0][i]), a1 = prepare_word<MODE>(v[1][i]);
+                        const uint32_t b0 = prepare_word<MODE>(v[2][i]), b1 = prepare_word<MODE>(v[3][i]);
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            const uint32_t x = tc::prmt(a0, a1, half ? 0x7362 : 0x5140), y = tc::prmt(b0, b1, half ? 0x7362 : 0x5140);
+                            mma_f16_16816(o[4 * i + 2 * half], pa[0], pa[1], pa[2], pa[3], pair_lo_h2<MODE>(x), pair_lo_h2<MODE>(y));
+                            mma_f16_16816(o[4 * i + 2 * half + 1], pa[0], pa[1], pa[2], pa[3], pair_hi_h2<MODE>(x), pair_hi_h2<MODE>(y));
+                        }
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&empty[stage]);
+                if (++stage == NS) { stage = 0; phase ^= 1; }
+            }
+            // join the four warps: references and sums first, then the outputs in warp order
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+                l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+                if (t4 == 0) {
+                    join_m[warp][g + 8 * r] = ref[r];
+                    join_l[warp][g + 8 * r] = bad[r] ? NAN : l[r];
+                }
+            }
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int row = g + 8 * r;
+                if (row >= m.rows) continue;
+                float top = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < kConsumers; ++i) top = fmaxf(top, join_m[i][row]);
+                const float f = top > -INFINITY ? exp2f(ref[r] - top) : 0.f;
+                float* dst = join + (warp * 16 + row) * D;
+#pragma unroll
+                for (int i = 0; i < NT; i += 4) {  // values (D / 8) (2 t4 + e) + i .. i + 3
+                    *reinterpret_cast<float4*>(dst + (D / 8) * (2 * t4) + i) =
+                        make_float4(o[i][2 * r] * f, o[i + 1][2 * r] * f, o[i + 2][2 * r] * f, o[i + 3][2 * r] * f);
+                    *reinterpret_cast<float4*>(dst + (D / 8) * (2 * t4 + 1) + i) = make_float4(
+                        o[i][2 * r + 1] * f, o[i + 1][2 * r + 1] * f, o[i + 2][2 * r + 1] * f, o[i + 3][2 * r + 1] * f);
+                }
+            }
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            // each warp finishes every fourth row
+            for (int row = warp; row < m.rows; row += kConsumers) {
+                float top = -INFINITY, sum = 0.f;
+#pragma unroll
+                for (int i = 0; i < kConsumers; ++i) top = fmaxf(top, join_m[i][row]);
+#pragma unroll
+                for (int i = 0; i < kConsumers; ++i)
+                    sum += join_l[i][row] * (join_m[i][row] > -INFINITY ? exp2f(join_m[i][row] - top) : (join_l[i][row] == 0.f ? 0.f : 1.f));
+                const float inv = sum > 0.f || sum != sum ? m.vmax / sum : 0.f;
+                const int f = m.f0 + row;
+                for (int d = lane * 4; d < D; d += 128) {
+                    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int i = 0; i < kConsumers; ++i) {
+                        const float4 y = *reinterpret_cast<const float4*>(join + (i * 16 + row) * D + d);
+                        x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
+                    }
+                    x.x *= inv; x.y *= inv; x.z *= inv; x.w *= inv;
+                    if (m.part < 0) {
+                        uint16_t* out = static_cast<uint16_t*>(p.a.out) +
+                                        ((m.row0 + f / G) * p.a.Hq + m.h * G + f % G) * D + d;
+                        *reinterpret_cast<uint2*>(out) = make_uint2(tc::f2_to_bf2(x.x, x.y), tc::f2_to_bf2(x.z, x.w));
+                    } else {
+                        const int64_t at = part_row(p, SeqSpan{m.row0, 0, 0, 0}, m.s, m.h, f) * p.max_chunks + m.chunk;
+                        *reinterpret_cast<float4*>(p.part_o + at * D + d) = x;
+                        if (d == 0) p.part_lse[at] = sum != sum ? 0.f : sum > 0.f ? top + log2f(sum) : -INFINITY;
+                    }
+                }
+            }
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            if (lane == 0) mbar_arrive(&meta_empty[slot]);
+        }
+    }
+}
+
+// Join the chunks of the rows whose sequence took several: one CTA per row of
+// partials, warp w sums chunks w, w + 4, ... in order, then the four sums.
+template <int D>
+__global__ void __launch_bounds__(128) kv_attn_join_kernel(const __grid_constant__ DecodeArgs p) {
+    __shared__ float sums[4][D];
+    __shared__ float weights[4];
+    pdl_launch_dependents();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int G = p.a.Hq / p.c.H;
+    int64_t t;
+    int s, hq;
+    if (p.row_limit > 0) {
+        const int f = static_cast<int>(blockIdx.x % p.row_limit);
+        const int64_t sh = blockIdx.x / p.row_limit;
+        s = static_cast<int>(sh / p.c.H);
+        hq = static_cast<int>(sh % p.c.H) * G + f % G;
+        t = clamped_start(p.st, s) + f / G;
+    } else {
+        t = blockIdx.x / p.a.Hq;
+        hq = static_cast<int>(blockIdx.x - t * p.a.Hq);
+        s = kv_find_seq(p.st, t, 1, 1, 0);
+    }
+    const SeqWork w = seq_work(p, s);
+    if (t < w.span.row0 || t >= w.span.row0 + w.span.n || w.tiles == 0 || w.chunks <= 1) return;
+    const int64_t at = static_cast<int64_t>(blockIdx.x) * p.max_chunks;
+    float top = -INFINITY;
+    for (int k = lane; k < w.chunks; k += 32) top = fmaxf(top, __ldcg(p.part_lse + at + k));
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (top == -INFINITY) top = 0.f;
+    constexpr int V = D / 32;  // values a lane
+    float acc[V] = {};
+    float weight = 0.f;
+#pragma unroll 4
+    for (int k = warp; k < w.chunks; k += 4) {
+        const float e = exp2f(__ldcg(p.part_lse + at + k) - top);
+        weight += e;
+#pragma unroll
+        for (int i = 0; i < V; i += 2) {
+            const float2 x = __ldcg(reinterpret_cast<const float2*>(p.part_o + (at + k) * D + lane * V + i));
+            acc[i] = fmaf(e, x.x, acc[i]);
+            acc[i + 1] = fmaf(e, x.y, acc[i + 1]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) sums[warp][lane * V + i] = acc[i];
+    if (lane == 0) weights[warp] = weight;
+    __syncthreads();
+    const float all = (weights[0] + weights[1]) + (weights[2] + weights[3]);
+    const float inv = all > 0.f ? 1.f / all : 0.f;
+    for (int d = threadIdx.x; d < D; d += 128)
+        static_cast<uint16_t*>(p.a.out)[(t * p.a.Hq + hq) * D + d] =
+            f32_to_bf16_bits(((sums[0][d] + sums[1][d]) + (sums[2][d] + sums[3][d])) * inv);
+}
+
+// K or V codes as [P * H][block][D] bytes, boxes of min(block, 64) tokens.
+bool code_map(CUtensorMap* map, const uint8_t* codes, const KvCache& c) {
+    EncodeTiled encode = tensor_map_encoder();
+    if (!encode) return false;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(c.D), static_cast<cuuint64_t>(c.block),
+                                static_cast<cuuint64_t>(c.P) * c.H};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(c.D), static_cast<cuuint64_t>(c.D) * c.block};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(c.D), static_cast<cuuint32_t>(c.block < kTile ? c.block : kTile), 1};
+    const cuuint32_t one[3] = {1, 1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(codes), dims, strides, box, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, c.D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int MODE, int D>
+cudaError_t launch(const DecodeArgs& p, int64_t part_rows, cudaStream_t stream, int num_sms) {
+    CUtensorMap kmap, vmap;
+    if (!code_map(&kmap, p.c.k_codes, p.c) || !code_map(&vmap, p.c.v_codes, p.c)) return cudaErrorInvalidValue;
+    constexpr int smem = 1024 + kStages<D> * 2 * kTile * D + kConsumers * 16 * D * 4;
+    cudaError_t e = cudaFuncSetAttribute(kv_attn_decode_kernel<MODE, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute pdl[1];
+    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    pdl[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    // one wave of resident CTAs, or as many as there can be items
+    const int64_t items = (p.st.rows * (p.a.Hq / p.c.H) / 16 + p.st.S) * p.max_chunks * p.c.H;
+    cfg.gridDim = dim3(static_cast<unsigned>(items < 2 * num_sms ? items : 2 * num_sms), 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = pdl;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kv_attn_decode_kernel<MODE, D>, p, kmap, vmap);
+    if (e != cudaSuccess || p.max_chunks <= 1) return e;
+    cfg.gridDim = dim3(static_cast<unsigned>(part_rows), 1, 1);
+    cfg.blockDim = dim3(128, 1, 1);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, kv_attn_join_kernel<D>, p);
+}
+
+}  // namespace
+
+unsigned int kv_attn_decode_error_take() { return pipeline_error_take(); }
+
+KvDecodePlan kv_decode_plan(const KvDecodeSizes& z, int num_sms) {
+    KvDecodePlan r{};
+    // two items for every resident CTA, if the sequences are long enough
+    const int64_t groups = z.S * z.H;
+    int64_t target = (4 * static_cast<int64_t>(num_sms) + groups - 1) / groups;
+    r.target = static_cast<int>(target < 1 ? 1 : target > 1 << 20 ? 1 << 20 : target);
+    const int64_t cap = z.max_pages * z.block;  // no sequence is longer
+    // chunks grow with the span, so the most there are is where the minimum or the maximum length binds
+    int64_t most = (cap + kChunkMax - 1) / kChunkMax;
+    const int64_t by_min = (cap + kChunkMin - 1) / kChunkMin;
+    const int64_t by_target = by_min < r.target ? by_min : r.target;
+    if (by_target > most) most = by_target;
+    r.max_chunks = static_cast<int>(most < 1 ? 1 : most);
+    r.row_limit = z.only ? 0 : 16;
+    r.part_rows = z.only ? z.rows * z.Hq : z.S * z.H * 16;
+    return r;
+}
+
+cudaError_t launch_kv_attn_decode(const KvAttn& a, const KvCache& c, const KvSteps& st, const KvDecodePlan& plan,
+                                  void* workspace, cudaStream_t stream, int num_sms) {
+    DecodeArgs p{a, c, st, plan.target, plan.max_chunks, plan.row_limit, nullptr, nullptr};
+    if (plan.max_chunks > 1) {
+        p.part_o = static_cast<float*>(workspace);
+        p.part_lse = p.part_o + plan.part_rows * plan.max_chunks * c.D;
+    }
+    if (c.D == 128)
+        return c.mode == NV_KV_INT8 ? launch<NV_KV_INT8, 128>(p, plan.part_rows, stream, num_sms)
+                                    : launch<NV_KV_E4M3, 128>(p, plan.part_rows, stream, num_sms);
+    return c.mode == NV_KV_INT8 ? launch<NV_KV_INT8, 64>(p, plan.part_rows, stream, num_sms)
+                                : launch<NV_KV_E4M3, 64>(p, plan.part_rows, stream, num_sms);
+}
+
+}  // namespace nvq
