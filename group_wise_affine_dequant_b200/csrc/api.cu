@@ -67,11 +67,33 @@ nv_status check_kv_pointers(const nvq::KvCache& c, const nvq::KvSteps& st) {
         if (!aligned4(p)) return NV_ERR_INVALID_ARG;
     return NV_OK;
 }
-// Which attention kernels a call takes: a pure function of the sizes.
-enum class KvRoute { kSimple, kDecode };
-KvRoute kv_attn_route(nv_dtype dt, int D, int64_t P, int64_t max_q, int64_t G) {
-    if (dt != NV_BF16 || (D != 64 && D != 128) || P == 0) return KvRoute::kSimple;
-    return max_q > 0 && max_q * G <= 16 ? KvRoute::kDecode : KvRoute::kSimple;
+// Which attention kernels a call takes, and their workspaces: a pure function of
+// the sizes. bf16 heads of 64 or 128 values have the tensor-core kernels: one for
+// sequences of at most 16 flattened rows (new tokens times heads of the group), one for more.
+// A call whose sequences may be of both kinds launches both, each leaves the other's alone.
+struct KvAttnPlan {
+    bool decode = false, prefill = false;
+    nvq::KvDecodePlan d{};
+    nvq::KvPrefillPlan p{};
+    size_t decode_bytes = 0, prefill_bytes = 0;
+};
+KvAttnPlan kv_attn_plan(nv_dtype dt, int64_t rows, int Hq, int H, int block, int D, int64_t max_pages,
+                        int64_t S, int64_t max_q, int sms) {
+    KvAttnPlan r;
+    if (dt != NV_BF16 || (D != 64 && D != 128)) return r;
+    const int64_t most = max_q > 0 && max_q < rows ? max_q : rows;
+    const bool only_few = most * (Hq / H) <= 16;
+    r.prefill = !only_few;
+    r.decode = only_few || S > 1;
+    if (r.decode) {
+        r.d = nvq::kv_decode_plan({rows, S, max_pages, Hq, H, block, D, only_few}, sms);
+        r.decode_bytes = (r.d.bytes(D) + 255) / 256 * 256;
+    }
+    if (r.prefill) {
+        r.p = nvq::kv_prefill_plan({rows, S, max_pages, Hq, H, block, D}, sms);
+        r.prefill_bytes = r.p.bytes(rows, Hq, D);
+    }
+    return r;
 }
 // A row stride in elements: the heads fit and every row starts on 16 bytes.
 bool valid_stride(int64_t stride, int64_t least, nv_dtype dt) {
@@ -384,8 +406,8 @@ size_t nv_kv_attention_workspace_size(nv_dtype dt, int64_t rows, int Hq, int H, 
     if (rows <= 0 || S <= 0 || max_pages < 0 || Hq < 1 || H < 1 || Hq % H || block < 1 || D < 1 || max_q < 0 ||
         rows > 0x7FFFFFFF || S > 0xFFFFFF || max_pages > 0x7FFFFFFF)
         return 0;
-    if (kv_attn_route(dt, D, 1, max_q, Hq / H) != KvRoute::kDecode) return 0;
-    return nvq::kv_decode_plan({rows, S, max_pages, Hq, H, block, D, true}, sm_count()).bytes(D);
+    const KvAttnPlan plan = kv_attn_plan(dt, rows, Hq, H, block, D, max_pages, S, max_q, sm_count());
+    return plan.decode_bytes + plan.prefill_bytes;
 }
 
 nv_status nv_kv_attention(const void* q, int64_t q_stride, nv_dtype dt, int64_t rows, int Hq,
@@ -412,10 +434,16 @@ nv_status nv_kv_attention(const void* q, int64_t q_stride, nv_dtype dt, int64_t 
     if (!q || !out || !aligned16(q) || !aligned16(out) || !valid_stride(q_stride, int64_t(Hq) * D, dt))
         return NV_ERR_INVALID_ARG;
     const nvq::KvAttn a{q, q_stride, out, dt, Hq, scale, causal != 0, window};
-    if (kv_attn_route(dt, D, P, max_q, Hq / H) == KvRoute::kDecode) {
-        const int sms = sm_count();
-        const nvq::KvDecodePlan plan = nvq::kv_decode_plan({rows, S, max_pages, Hq, H, block, D, true}, sms);
-        return from_cuda(nvq::launch_kv_attn_decode(a, c, steps, plan, workspace, stream, sms));
+    const int sms = sm_count();
+    const KvAttnPlan plan = kv_attn_plan(dt, rows, Hq, H, block, D, max_pages, S, max_q, sms);
+    if (P > 0 && (plan.decode || plan.prefill)) {
+        if (plan.decode) {
+            st = from_cuda(nvq::launch_kv_attn_decode(a, c, steps, plan.d, workspace, stream, sms));
+            if (st != NV_OK) return st;
+        }
+        if (!plan.prefill) return NV_OK;
+        return from_cuda(nvq::launch_kv_attn_prefill(a, c, steps, plan.p, plan.decode ? plan.d.row_limit : 0,
+                                                     static_cast<char*>(workspace) + plan.decode_bytes, stream));
     }
     return from_cuda(nvq::launch_kv_attn_simple(a, c, steps, stream));
 }
@@ -443,10 +471,11 @@ nv_status nv_pipeline_error(uint32_t* host_code) {
     const unsigned int g = nvq::tc_gather_t0_error_take();
     const unsigned int t = nvq::selftest_error_take();
     const unsigned int kd = nvq::kv_attn_decode_error_take();
+    const unsigned int kp = nvq::kv_attn_prefill_error_take();
     if (a == 0xFFFFFFFFu || b == 0xFFFFFFFFu || c == 0xFFFFFFFFu || d == 0xFFFFFFFFu ||
-        g == 0xFFFFFFFFu || t == 0xFFFFFFFFu || kd == 0xFFFFFFFFu)
+        g == 0xFFFFFFFFu || t == 0xFFFFFFFFu || kd == 0xFFFFFFFFu || kp == 0xFFFFFFFFu)
         return NV_ERR_CUDA;
-    *host_code = a ? a : b ? b : c ? c : d ? d : g ? g : kd ? kd : t;
+    *host_code = a ? a : b ? b : c ? c : d ? d : g ? g : kd ? kd : kp ? kp : t;
     return NV_OK;
 }
 

@@ -148,4 +148,22 @@ cudaError_t launch_kv_attn_decode(const KvAttn& a, const KvCache& c, const KvSte
                                   void* workspace, cudaStream_t stream, int num_sms);
 unsigned int kv_attn_decode_error_take();
 
+// Tensor-core kernel for many rows a sequence (bf16, D 64 or 128); sequences of at
+// most row_min flattened rows are left to the other.
+struct KvPrefillSizes {
+    int64_t rows, S, max_pages;
+    int Hq, H, block, D;
+};
+struct KvPrefillPlan {
+    int64_t items;
+    int splits;
+    size_t bytes(int64_t rows, int Hq, int D) const {
+        return splits > 1 ? static_cast<size_t>(rows) * Hq * splits * (D + 1) * sizeof(float) : 0;
+    }
+};
+KvPrefillPlan kv_prefill_plan(const KvPrefillSizes& z, int num_sms);
+cudaError_t launch_kv_attn_prefill(const KvAttn& a, const KvCache& c, const KvSteps& st, const KvPrefillPlan& plan,
+                                   int row_min, void* workspace, cudaStream_t stream);
+unsigned int kv_attn_prefill_error_take();
+
 }  // namespace nvq

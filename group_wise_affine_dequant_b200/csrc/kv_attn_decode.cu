@@ -236,7 +236,7 @@ kv_attn_decode_kernel(const __grid_constant__ DecodeArgs p, const __grid_constan
             for (int i = 0; i < (kBlocksMax + 31) / 32; ++i) {
                 const int b = lane + 32 * i;
                 if (b < blocks) {
-                    const float lg = vs_of[i] > 0.f ? fmaxf(log2f(vs_of[i]) - log2f(vmax), -100.f) : 0.f;
+                    const float lg = vs_of[i] > 0.f ? fmaxf(log2f(vs_of[i]) - log2f(vmax), kLgMin) : kLgMin;
                     scales[slot][b].lg = lg;
                     scales[slot][b].inv = exp2f(-lg);
                 }

@@ -1,0 +1,621 @@
+// Attention over the paged 8-bit cache for many query rows a sequence (bf16, 64 or
+// 128 values a head), on the tensor cores (tcgen05).
+//
+// An item is 256 query rows of one sequence and key/value head (row = (token,
+// query head of the group)) against its visible tokens, 128 at a time. One CTA per
+// SM and item; rows form two subtiles of 128 that share every converted key and
+// value tile and take turns on the tensor core: while one subtile's softmax runs, the
+// other's products do.
+//   warps 0-3, 4-7   softmax of subtile 0, 1: thread = row = TMEM lane; scores
+//                    arrive in TMEM, weights go back over them as fp16
+//   warps 8-11       converters: 8-bit codes from global memory (the next tile's
+//                    loads are in flight while this one's are converted), exact
+//                    fp16 into swizzled shared tiles [token][value], a ring of two
+//                    K and two V tiles
+//   warp 12          issues the products: S = Q K^T (K-major operands), O += P V
+//                    with P from TMEM and V read along tokens (MN-major), so V
+//                    needs no transpose
+// TMEM (512 columns): S0, S1 (128 each, P over the first 64), O0, O1 (D each).
+//
+// Block scales never touch the tiles: keys' are factors of the scores, values' join
+// the exponent (weights are 2^(z + lg)), and the weights' sum takes them out again.
+// A row's reference follows its running maximum only when that passes it by
+// kSlack, so rescaling O in TMEM is rare and the softmax warps do it themselves.
+//
+// Bound: the tensor core (4 * D flops a pair) together with the exponentials
+// (16 a clock and SM: 128 x 128 scores cost as many clocks as their two products).
+#include <cstdint>
+
+#include "kv_mma.cuh"
+
+namespace nvq {
+namespace {
+
+constexpr int kRows = 256;     // rows an item
+constexpr int kTile = 128;     // tokens a tile
+constexpr int kThreads = 512;
+constexpr int kTmemCols = 512;
+constexpr int kMeta = 4;       // ring of per-tile scales
+
+// Registers a thread by role: the block starts with kThreads * kRegsLaunch and the
+// shares must not sum to more (a share that cannot be had would wait forever).
+constexpr int kRegsLaunch = 128, kRegsSoftmax = 176, kRegsConvert = 104, kRegsIssue = 48;
+static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsConvert + 128 * kRegsIssue <= kThreads * kRegsLaunch, "");
+
+struct PrefillArgs {
+    KvAttn a;
+    KvCache c;
+    KvSteps st;
+    int64_t items;    // row tiles of all sequences, at most
+    int splits;       // parts the tokens of an item are cut into
+    int row_min;      // sequences of at most this many flattened rows are another kernel's
+    float* part_o;    // [rows * Hq][splits][D]
+    float* part_lse;  // [rows * Hq][splits]
+};
+
+struct TileScales {  // of 16 tokens
+    float ks;   // negative: not seen
+    float lg, inv;
+    float pad;
+};
+
+__device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, uint32_t* v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+          "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+          "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+        "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+        "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
+}
+// fp16 operands, fp32 accumulator; b_mn: B is read along N (MN-major).
+__host__ __device__ constexpr uint32_t idesc_f16(int m, int n, int b_mn) {
+    return (1u << 4) | (static_cast<uint32_t>(b_mn) << 16) | (static_cast<uint32_t>(n >> 3) << 17) |
+           (static_cast<uint32_t>(m >> 4) << 24);
+}
+// MN-major, 128-byte swizzle: rows of 64 values; 8-token groups 1024 bytes apart
+// (stride offset), the next 64 values `lead` bytes on (leading offset).
+__device__ __forceinline__ uint64_t sw128_mn_desc(const void* p, uint32_t lead) {
+    const uint64_t addr = smem_u32(p);
+    return ((addr & 0x3FFFFull) >> 4) | (static_cast<uint64_t>(lead >> 4) << 16) |
+           (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+// Byte offset of 16-byte piece `piece` (8 values) of row r in a [rows][64 values] swizzled tile.
+__device__ __forceinline__ uint32_t sw128_at(int r, int piece) {
+    return static_cast<uint32_t>((r >> 3) * 1024 + (r & 7) * 128 + ((piece ^ (r & 7)) << 4));
+}
+
+template <int D>
+struct Smem {
+    static constexpr int kHalves = D / 64;
+    static constexpr int kHalf = 128 * 128;               // bytes of 128 rows x 64 values
+    static constexpr int kSub = kHalves * kHalf;          // a Q subtile, a K or V tile
+    static constexpr int kSlots = 4;                      // K, V, K, V
+    static constexpr int kBytes = (2 + kSlots) * kSub + 1024;
+};
+
+template <int MODE, int D>
+__global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __grid_constant__ PrefillArgs p) {
+    using L = Smem<D>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    uint8_t* q_smem = smem;                      // [2][kSub]
+    uint8_t* ring = smem + 2 * L::kSub;          // [4][kSub]
+    __shared__ __align__(8) uint64_t full[4], empty[4], q_full[2], s_full[2], p_full[2], o_full[2], m_full[kMeta];
+    __shared__ TileScales scales[kMeta][kTile / 16];
+    __shared__ uint32_t tmem_slot, vmax_bits;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+    if (tid == 0) {
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&full[i], 128);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&q_full[i], 128);
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 128);
+            mbar_init(&o_full[i], 1);
+        }
+        for (int i = 0; i < kMeta; ++i) mbar_init(&m_full[i], 1);
+        mbar_init_fence();
+        vmax_bits = 0;
+    }
+    pdl_launch_dependents();
+    pdl_wait();
+
+    // ---- the item: later rows first, they see the most tokens
+    const int G = p.a.Hq / p.c.H;
+    const int h = blockIdx.x % p.c.H;
+    const int64_t item = p.items - 1 - blockIdx.x / p.c.H;
+    const int s = kv_find_seq(p.st, item, G, kRows, 1);
+    const SeqSpan span = seq_span(p.st, s, p.c.block);
+    const int64_t j_item = item - kv_first_item(p.st, s, G, kRows, 1);
+    const int64_t seq_rows = static_cast<int64_t>(span.n) * G;
+    if (j_item < 0 || j_item * kRows >= seq_rows || seq_rows <= p.row_min) return;
+    const int f0 = static_cast<int>(j_item * kRows);
+    const int rows = seq_rows - f0 < kRows ? static_cast<int>(seq_rows - f0) : kRows;
+    int lo = 0, hi = span.len;
+    if (p.a.causal) {
+        const int p0 = span.first + f0 / G, p1 = span.first + (f0 + rows - 1) / G;
+        hi = p1 + 1 < hi ? p1 + 1 : hi;
+        if (p.a.window > 0 && p0 + 1 > p.a.window) lo = p0 + 1 - p.a.window;
+    }
+    lo = lo / kTile * kTile;
+    int tiles = hi > lo ? (hi - lo + kTile - 1) / kTile : 0;
+    if (p.splits > 1) {
+        const int per = (tiles + p.splits - 1) / p.splits;
+        const int z = blockIdx.y;
+        lo += z * per * kTile;
+        tiles = tiles - z * per < per ? tiles - z * per : per;
+        if (tiles < 0) tiles = 0;
+        if (lo + tiles * kTile < hi) hi = lo + tiles * kTile;
+    }
+
+    // ---- the largest value scale of the item: weights carry value scales relative to it
+    if (tiles > 0) {
+        const int b0 = lo / p.c.block, b1 = (hi - 1) / p.c.block;
+        float most = 0.f;
+        for (int b = b0 + tid; b <= b1; b += kThreads) {
+            const int32_t page = __ldg(p.st.pages + static_cast<int64_t>(s) * p.st.max_pages + b);
+            if (page >= 0 && page < p.c.P) most = fmaxf(most, __ldg(p.c.v_scales + static_cast<int64_t>(page) * p.c.H + h));
+        }
+        __syncthreads();  // vmax_bits initialised
+        const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(most));
+        if (lane == 0 && bits) atomicMax(&vmax_bits, bits);
+    }
+    if (warp == 12) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)),
+                     "r"(kTmemCols));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    const float vmax = __uint_as_float(vmax_bits);
+    bool ok = true;
+
+    if (warp < 8) {
+        // ------------------------------------------------------------- softmax
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+        const int sub = warp >> 2;
+        const int r_sub = tid & 127;              // row of the subtile = TMEM lane
+        const int row = sub * 128 + r_sub;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t s_at = tmem + lanes + static_cast<uint32_t>(sub * 128);
+        const uint32_t o_at = tmem + lanes + 256u + static_cast<uint32_t>(sub * D);
+        const int f = f0 + row, tok = f / G;
+        int row_lo = 0, row_hi = span.len;
+        float zc = 0.f;
+        bool bad = false;
+        int64_t out_row = 0;
+        {
+            uint4 raw[D / 8];
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) raw[i] = make_uint4(0, 0, 0, 0);
+            if (row < rows) {
+                const int pos = span.first + tok;
+                if (p.a.causal) {
+                    row_hi = pos + 1 < span.len ? pos + 1 : span.len;
+                    if (p.a.window > 0 && pos + 1 > p.a.window) row_lo = pos + 1 - p.a.window;
+                }
+                const int hq = h * G + f % G;
+                out_row = (span.row0 + tok) * p.a.Hq + hq;
+                const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.a.q) +
+                                                                (span.row0 + tok) * p.a.q_stride + static_cast<int64_t>(hq) * D);
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) raw[i] = __ldg(q + i);
+            }
+            uint32_t most = 0;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                const uint32_t u[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) most = max(most, max((u[j] << 16) & 0x7FFFFFFFu, u[j] & 0x7FFF0000u));
+            }
+            bad = most >= 0x7F800000u;
+            const uint32_t ex = row_exponent(most);
+            // a negative scale goes into the queries: scores times zc keep their order
+            const float down = p.a.scale < 0.f ? -pow2_bits(254u - ex) : pow2_bits(254u - ex);
+            zc = fabsf(p.a.scale) * kLog2e * pow2_bits(ex);
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                const uint32_t u[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+                uint32_t x[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    x[j] = f2_to_h2(__uint_as_float(u[j] << 16) * down, __uint_as_float(u[j] & 0xFFFF0000u) * down);
+                *reinterpret_cast<uint4*>(q_smem + sub * L::kSub + (i >> 3) * L::kHalf + sw128_at(r_sub, i & 7)) =
+                    make_uint4(x[0], x[1], x[2], x[3]);
+            }
+            fence_proxy_async();
+            mbar_arrive(&q_full[sub]);
+        }
+        float ref = -INFINITY, l = 0.f;
+        for (int i = 0; ok && i < tiles; ++i) {
+            const int j0 = lo + i * kTile;
+            ok = mbar_wait(&m_full[i & (kMeta - 1)], (i / kMeta) & 1, 0x71) && mbar_wait(&s_full[sub], i & 1, 0x72);
+            if (!ok) break;
+            tc::tc_fence_after();
+            uint32_t sr[128];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld_x32(s_at + 32u * c, sr + 32 * c);
+            tmem_ld_wait();
+            const TileScales* ts = scales[i & (kMeta - 1)];
+            float k[8];
+            bool all = row_lo <= j0 && row_hi >= j0 + kTile;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                k[c] = ts[c].ks;
+                all &= k[c] >= 0.f;
+                k[c] *= zc;
+            }
+            float mx = -INFINITY;
+            if (__all_sync(0xffffffffu, all)) {
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    float m = __uint_as_float(sr[16 * c]);
+#pragma unroll
+                    for (int e = 1; e < 16; ++e) m = fmaxf(m, __uint_as_float(sr[16 * c + e]));
+                    mx = fmaxf(mx, fmaf(m, k[c], ts[c].lg));
+                }
+            } else {  // some rows of the warp do not see all of the tile
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const bool seen = ts[c].ks >= 0.f;
+                    float m = -INFINITY;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const int j = j0 + 16 * c + e;
+                        float z = __uint_as_float(sr[16 * c + e]) * k[c];
+                        if (!seen || j < row_lo || j >= row_hi) z = -INFINITY;
+                        sr[16 * c + e] = __float_as_uint(z);
+                        m = fmaxf(m, z);
+                    }
+                    k[c] = 1.f;
+                    mx = fmaxf(mx, m + ts[c].lg);
+                }
+            }
+            const bool up = mx > ref + kSlack;
+            if (__any_sync(0xffffffffu, up)) {
+                // each row by itself; the previous tile's P V is complete (its commit came before this S)
+                const float fct = up ? exp2f(ref - mx) : 1.f;
+                ref = up ? mx : ref;
+                l *= fct;
+                if (i > 0) {
+#pragma unroll
+                    for (int c = 0; c < D / 16; ++c) {
+                        uint32_t ov[16];
+                        asm volatile(
+                            "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+                            "%12, %13, %14, %15}, [%16];"
+                            : "=r"(ov[0]), "=r"(ov[1]), "=r"(ov[2]), "=r"(ov[3]), "=r"(ov[4]), "=r"(ov[5]), "=r"(ov[6]),
+                              "=r"(ov[7]), "=r"(ov[8]), "=r"(ov[9]), "=r"(ov[10]), "=r"(ov[11]), "=r"(ov[12]),
+                              "=r"(ov[13]), "=r"(ov[14]), "=r"(ov[15])
+                            : "r"(o_at + 16u * c));
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * fct);
+                        tc::tmem_st_x16_async(o_at + 16u * c, ov);
+                    }
+                    tc::tmem_st_wait();
+                }
+            }
+            const float minus_ref = kLift - (ref > -INFINITY ? ref : 0.f);
+            uint32_t pw[64];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                const float base = ts[c].lg + minus_ref;
+                float sum = 0.f;
+#pragma unroll
+                for (int e = 0; e < 16; e += 2) {
+                    const float w0 = exp2_approx(fmaf(__uint_as_float(sr[16 * c + e]), k[c], base));
+                    const float w1 = exp2_approx(fmaf(__uint_as_float(sr[16 * c + e + 1]), k[c], base));
+                    sum += w0 + w1;
+                    pw[8 * c + e / 2] = f2_to_h2(w0, w1);
+                }
+                l = fmaf(sum, ts[c].inv, l);
+            }
+            tmem_st_x32(s_at, pw);
+            tmem_st_x32(s_at + 32u, pw + 32);
+            tc::tmem_st_wait();
+            tc::tc_fence_before();
+            mbar_arrive(&p_full[sub]);
+        }
+        // ---- output
+        if (ok && tiles > 0) ok = mbar_wait(&o_full[sub], 0, 0x73);
+        tc::tc_fence_after();
+        if (ok) {
+            const bool live = row < rows;
+            const float inv = bad ? NAN : l > 0.f || l != l ? vmax / l : 0.f;
+            const int64_t at = p.splits > 1 ? out_row * p.splits + blockIdx.y : 0;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t ov[32];
+                if (tiles > 0) {
+                    tmem_ld_x32(o_at + 32u * c, ov);
+                    tmem_ld_wait();
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) ov[e] = 0;
+                }
+                if (!live) continue;
+                if (p.splits > 1) {
+                    float4* o = reinterpret_cast<float4*>(p.part_o + at * D + 32 * c);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        o[e] = make_float4(__uint_as_float(ov[4 * e]) * inv, __uint_as_float(ov[4 * e + 1]) * inv,
+                                           __uint_as_float(ov[4 * e + 2]) * inv, __uint_as_float(ov[4 * e + 3]) * inv);
+                } else {
+                    uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.a.out) + out_row * D + 32 * c);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t x[4];
+#pragma unroll
+                        for (int n = 0; n < 4; ++n)
+                            x[n] = tc::f2_to_bf2(__uint_as_float(ov[8 * e + 2 * n]) * inv, __uint_as_float(ov[8 * e + 2 * n + 1]) * inv);
+                        o[e] = make_uint4(x[0], x[1], x[2], x[3]);
+                    }
+                }
+            }
+            if (live && p.splits > 1)
+                p.part_lse[at] = bad || l != l ? 0.f : l > 0.f ? ref - kLift + log2f(l) : -INFINITY;
+        }
+        tc::tc_fence_before();
+    } else if (warp < 12) {
+        // ---------------------------------------------------------- converters
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConvert));
+        const int ct = tid - 256;
+        constexpr int kVecs = D / 16;                 // 16-byte pieces of codes a token
+        constexpr int kStep = 128 / kVecs;            // tokens a pass of the 128 threads
+        constexpr int kPasses = kTile / kStep;        // 8 (D 128) or 4 (D 64)
+        const int vec = ct % kVecs, tok0 = ct / kVecs;
+        // byte offset of (token tok0 + kStep n) in the tile's codes, by pass; -1: nothing there
+        int64_t at[kPasses];
+        auto places = [&](int i) {
+            const int j0 = lo + i * kTile;
+#pragma unroll
+            for (int n = 0; n < kPasses; ++n) {
+                const int j = j0 + tok0 + kStep * n;
+                at[n] = -1;
+                if (j < hi) {
+                    const int b = j / p.c.block;
+                    const int32_t page = __ldg(p.st.pages + static_cast<int64_t>(s) * p.st.max_pages + b);
+                    if (page >= 0 && page < p.c.P)
+                        at[n] = ((static_cast<int64_t>(page) * p.c.H + h) * p.c.block + (j - b * p.c.block)) * D + 16 * vec;
+                }
+            }
+        };
+        auto load = [&](const uint8_t* codes, uint4 (&raw)[kPasses]) {
+#pragma unroll
+            for (int n = 0; n < kPasses; ++n)
+                raw[n] = at[n] >= 0 ? __ldg(reinterpret_cast<const uint4*>(codes + at[n])) : make_uint4(0, 0, 0, 0);
+        };
+        auto convert = [&](const uint4 (&raw)[kPasses], uint8_t* tile) {
+#pragma unroll
+            for (int n = 0; n < kPasses; ++n) {
+                const uint32_t x[4] = {raw[n].x, raw[n].y, raw[n].z, raw[n].w};
+                uint4 y[2];
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    const uint32_t a = prepare_word<MODE>(x[2 * m]), b = prepare_word<MODE>(x[2 * m + 1]);
+                    y[m] = make_uint4(pair_lo_h2<MODE>(a), pair_hi_h2<MODE>(a), pair_lo_h2<MODE>(b), pair_hi_h2<MODE>(b));
+                }
+                const int r = tok0 + kStep * n;
+                uint8_t* half = tile + (vec >> 2) * L::kHalf;
+                // threads of the two halves store their two pieces in opposite order: no bank conflicts
+                const int swap = (vec >> 2) & 1;
+                *reinterpret_cast<uint4*>(half + sw128_at(r, 2 * (vec & 3) + swap)) = swap ? y[1] : y[0];
+                *reinterpret_cast<uint4*>(half + sw128_at(r, 2 * (vec & 3) + 1 - swap)) = swap ? y[0] : y[1];
+            }
+            fence_proxy_async();
+        };
+        uint4 kraw[kPasses], vraw[kPasses];
+        if (tiles > 0) {
+            places(0);
+            load(p.c.k_codes, kraw);
+        }
+        for (int i = 0; ok && i < tiles; ++i) {
+            load(p.c.v_codes, vraw);
+            if (ct < kTile / 16) {  // scales of 16 tokens each
+                const int j = lo + i * kTile + 16 * ct;
+                TileScales t{-1.f, 0.f, 1.f, 0.f};
+                if (j < hi) {
+                    const int page = page_of(p.st, p.c, s, j / p.c.block);
+                    if (page >= 0) {
+                        const int64_t ph = static_cast<int64_t>(page) * p.c.H + h;
+                        const float vs = __ldg(p.c.v_scales + ph);
+                        t.ks = __ldg(p.c.k_scales + ph);
+                        t.lg = vs > 0.f ? fmaxf(log2f(vs) - log2f(vmax), kLgMin) : kLgMin;
+                        t.inv = exp2f(-t.lg);
+                    }
+                }
+                scales[i & (kMeta - 1)][ct] = t;
+            }
+            if (warp == 8) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&m_full[i & (kMeta - 1)]);
+            }
+            const int ks = 2 * (i & 1), vs = ks + 1;
+            const uint32_t free_parity = ((i >> 1) & 1) ^ 1;
+            ok = mbar_wait(&empty[ks], free_parity, 0x74);
+            if (!ok) break;
+            convert(kraw, ring + ks * L::kSub);
+            mbar_arrive(&full[ks]);
+            if (i + 1 < tiles) {
+                places(i + 1);
+                load(p.c.k_codes, kraw);
+            }
+            ok = mbar_wait(&empty[vs], free_parity, 0x75);
+            if (!ok) break;
+            convert(vraw, ring + vs * L::kSub);
+            mbar_arrive(&full[vs]);
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+        if (warp == 12 && lane == 0 && tiles > 0) {
+            // ------------------------------------------------------ the products
+            constexpr uint32_t idesc_s = idesc_f16(128, kTile, 0), idesc_o = idesc_f16(128, D, 1);
+            auto qk = [&](int sub, int i) {
+                const uint64_t a = tc::sw128_desc(q_smem + sub * L::kSub), b = tc::sw128_desc(ring + 2 * (i & 1) * L::kSub);
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint64_t off = static_cast<uint64_t>(((k >> 2) * L::kHalf + (k & 3) * 32) >> 4);
+                    tc::tc_mma(tmem + sub * 128, a + off, b + off, idesc_s, k > 0);
+                }
+            };
+            auto pv = [&](int sub, int i) {
+                const uint64_t b = sw128_mn_desc(ring + (2 * (i & 1) + 1) * L::kSub, L::kHalf);
+#pragma unroll
+                for (int k = 0; k < kTile / 16; ++k)
+                    tc::tc_mma_ts(tmem + 256 + sub * D, tmem + sub * 128 + 8 * k, b + static_cast<uint64_t>(k * 2048 >> 4), idesc_o,
+                                  i > 0 || k > 0);
+            };
+            ok = mbar_wait(&full[0], 0, 0x76);
+            for (int sub = 0; ok && sub < 2; ++sub) {
+                ok = mbar_wait(&q_full[sub], 0, 0x77);
+                if (!ok) break;
+                tc::tc_fence_after();
+                qk(sub, 0);
+                tc::tc_commit(&s_full[sub]);
+            }
+            if (ok) tc::tc_commit(&empty[0]);
+            for (int i = 0; ok && i < tiles; ++i) {
+                const uint32_t ph = (i >> 1) & 1, phn = ((i + 1) >> 1) & 1;
+                const int ks = 2 * ((i + 1) & 1), vs = 2 * (i & 1) + 1;
+                for (int sub = 0; ok && sub < 2; ++sub) {
+                    ok = mbar_wait(&p_full[sub], i & 1, 0x78) && (sub || mbar_wait(&full[vs], ph, 0x79));
+                    if (!ok) break;
+                    tc::tc_fence_after();
+                    pv(sub, i);
+                    if (i + 1 == tiles) tc::tc_commit(&o_full[sub]);
+                    if (sub) tc::tc_commit(&empty[vs]);
+                    if (i + 1 < tiles) {
+                        if (!sub) {
+                            ok = mbar_wait(&full[ks], phn, 0x7A);
+                            if (!ok) break;
+                            tc::tc_fence_after();
+                        }
+                        qk(sub, i + 1);
+                        tc::tc_commit(&s_full[sub]);
+                        if (sub) tc::tc_commit(&empty[ks]);
+                    }
+                }
+            }
+        }
+        __syncwarp();
+    }
+    __syncthreads();
+    if (warp == 12) {
+        tc::tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
+    }
+}
+
+// Join the parts of every row: one warp per (row, query head), parts in order.
+template <int D>
+__global__ void __launch_bounds__(128) kv_attn_prefill_join_kernel(const __grid_constant__ PrefillArgs p) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const int lane = threadIdx.x & 31;
+    const int64_t at = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+    if (at >= p.st.rows * p.a.Hq) return;
+    const int64_t t = at / p.a.Hq;
+    const int s = kv_find_seq(p.st, t, 1, 1, 0);
+    const SeqSpan span = seq_span(p.st, s, p.c.block);
+    if (t < span.row0 || t >= span.row0 + span.n || static_cast<int64_t>(span.n) * (p.a.Hq / p.c.H) <= p.row_min) return;
+    float top = -INFINITY;
+    for (int k = lane; k < p.splits; k += 32) top = fmaxf(top, __ldcg(p.part_lse + at * p.splits + k));
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (top == -INFINITY) top = 0.f;
+    constexpr int V = D / 32;
+    float acc[V] = {}, all = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < p.splits; ++k) {
+        const float e = exp2f(__ldcg(p.part_lse + at * p.splits + k) - top);
+        all += e;
+#pragma unroll
+        for (int i = 0; i < V; i += 2) {
+            const float2 x = __ldcg(reinterpret_cast<const float2*>(p.part_o + (at * p.splits + k) * D + lane * V + i));
+            acc[i] = fmaf(e, x.x, acc[i]);
+            acc[i + 1] = fmaf(e, x.y, acc[i + 1]);
+        }
+    }
+    const float inv = all > 0.f ? 1.f / all : 0.f;
+    uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.a.out) + at * D + lane * V);
+#pragma unroll
+    for (int i = 0; i < V; i += 2) out[i / 2] = tc::f2_to_bf2(acc[i] * inv, acc[i + 1] * inv);
+}
+
+template <int MODE, int D>
+cudaError_t launch(const PrefillArgs& p, cudaStream_t stream) {
+    cudaError_t e = cudaFuncSetAttribute(kv_attn_prefill_kernel<MODE, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         Smem<D>::kBytes);
+    if (e != cudaSuccess) return e;
+    // the register shares are taken from what the block is launched with
+    static const int regs = [] {
+        cudaFuncAttributes at{};
+        return cudaFuncGetAttributes(&at, kv_attn_prefill_kernel<MODE, D>) == cudaSuccess ? at.numRegs : 0;
+    }();
+    if (regs < kRegsLaunch) return cudaErrorLaunchOutOfResources;
+    cudaLaunchAttribute pdl[1];
+    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    pdl[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.items * p.c.H), p.splits, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = Smem<D>::kBytes;
+    cfg.stream = stream;
+    cfg.attrs = pdl;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kv_attn_prefill_kernel<MODE, D>, p);
+    if (e != cudaSuccess || p.splits <= 1) return e;
+    cfg.gridDim = dim3(static_cast<unsigned>((p.st.rows * p.a.Hq + 3) / 4), 1, 1);
+    cfg.blockDim = dim3(128, 1, 1);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, kv_attn_prefill_join_kernel<D>, p);
+}
+
+}  // namespace
+
+unsigned int kv_attn_prefill_error_take() { return pipeline_error_take(); }
+
+KvPrefillPlan kv_prefill_plan(const KvPrefillSizes& z, int num_sms) {
+    KvPrefillPlan r{};
+    r.items = kv_items(z.rows, static_cast<int>(z.S), z.Hq / z.H, kRows, 1);
+    // few row tiles: cut the tokens, down to two tiles of them a part
+    const int64_t ctas = r.items * z.H;
+    const int64_t tiles = (z.max_pages * z.block + kTile - 1) / kTile;
+    int64_t splits = num_sms / (ctas > 0 ? ctas : 1);
+    if (splits > tiles / 2) splits = tiles / 2;
+    r.splits = static_cast<int>(splits < 1 ? 1 : splits);
+    return r;
+}
+
+cudaError_t launch_kv_attn_prefill(const KvAttn& a, const KvCache& c, const KvSteps& st, const KvPrefillPlan& plan,
+                                   int row_min, void* workspace, cudaStream_t stream) {
+    PrefillArgs p{a, c, st, plan.items, plan.splits, row_min, nullptr, nullptr};
+    if (plan.splits > 1) {
+        p.part_o = static_cast<float*>(workspace);
+        p.part_lse = p.part_o + st.rows * a.Hq * plan.splits * c.D;
+    }
+    if (c.D == 128)
+        return c.mode == NV_KV_INT8 ? launch<NV_KV_INT8, 128>(p, stream) : launch<NV_KV_E4M3, 128>(p, stream);
+    return c.mode == NV_KV_INT8 ? launch<NV_KV_INT8, 64>(p, stream) : launch<NV_KV_E4M3, 64>(p, stream);
+}
+
+}  // namespace nvq

@@ -119,11 +119,12 @@ def read(raw, scales, step: Step, mode: str, s: int, upto=None):
 
 
 def attention(q, kraw, ks, vraw, vs, step: Step, mode: str, scale, causal=True, window=0, drop=None):
-    """float64 (out, a, dz): a = sum_j p_j |v_j|, dz the largest sum_d |scale q_d k_jd| a row
-    sees (what fp32 rounding of its scores is a share of). drop(s, j): tokens not seen."""
+    """float64 (out, a, dz, small): a = sum_j p_j |v_j|, dz the largest sum_d |scale q_d k_jd| a row
+    sees (what fp32 rounding of its scores is a share of), small = max_j (p_j * value scale) *
+    sum_j |value code_j| over what it sees. drop(s, j): tokens not seen."""
     T, Hq, D = q.shape
     H = kraw.shape[1]
-    out, a = torch.zeros(T, Hq, D, dtype=torch.float64), torch.zeros(T, Hq, D, dtype=torch.float64)
+    out, a, small = (torch.zeros(T, Hq, D, dtype=torch.float64) for _ in range(3))
     dz = torch.zeros(T, Hq, 1, dtype=torch.float64)
     for s, (n, m) in enumerate(zip(step.lens, step.news)):
         if m == 0:
@@ -132,6 +133,9 @@ def attention(q, kraw, ks, vraw, vs, step: Step, mode: str, scale, causal=True, 
         if n == 0:
             continue
         k, v = read(kraw, ks, step, mode, s), read(vraw, vs, step, mode, s)
+        codes = read(vraw, torch.ones_like(vs), step, mode, s).abs()
+        ids = step.pages[s, : -(-n // step.block)].long()
+        v_scale = vs[ids].double().repeat_interleave(step.block, 0)[:n]
         place = torch.arange(n)[None]
         rows = torch.arange(n - m, n)[:, None]
         seen = place <= rows if causal else torch.ones(m, n, dtype=torch.bool)
@@ -151,11 +155,12 @@ def attention(q, kraw, ks, vraw, vs, step: Step, mode: str, scale, causal=True, 
             out[r0:r0 + m, h] = p @ v[:, kv]
             a[r0:r0 + m, h] = p @ v[:, kv].abs()
             dz[r0:r0 + m, h, 0] = size.amax(1)
-    return out, a, dz
+            small[r0:r0 + m, h] = (p * v_scale[:, kv]).amax(1, keepdim=True) * (seen.double() @ codes[:, kv])
+    return out, a, dz, small
 
 
-def attention_tolerance(out, a, dz, dtype, D, tokens):
-    """|got - out| allowed, from the arithmetic alone.
+def attention_tolerance(out, terms, dtype, D, tokens):
+    """|got - out| allowed, from the arithmetic alone; terms as attention() gives them.
 
     A score is a sum of D products in fp32 (any order: at most D + 4 roundings of
     2^-24 of its terms' sum, with the scale, the base-2 factor and the
@@ -163,8 +168,12 @@ def attention_tolerance(out, a, dz, dtype, D, tokens):
     2 (D + 8) 2^-24 dz at most, numerator and denominator alike; the
     exponential costs 2^-22, the sums over tokens (tokens + 64) 2^-24 each, by
     pieces of 16 and more at a time: no more than 64 + tokens / 16 steps. bf16 calls round
-    the weights to 11 bits (2^-12 each, in the numerator) and the result to bf16 (2^-8)."""
+    the weights to 11 bits (2^-12 each, in the numerator) and the result to bf16 (2^-8).
+    A weight times its value scale is rounded as an fp16 number that is at least 2^8 for
+    the row's largest, so where it is subnormal its error is 2^-25 instead, 2^-33 of
+    that largest: in all 2^-33 of `small`."""
+    a, dz, small = terms
     share = 2 * 2 * (D + 8) * 2.0 ** -24 * dz + 2.0 ** -21 + 2 * (64 + tokens / 16) * 2.0 ** -24
     if dtype == torch.float32:
         return a * share + out.abs() * 2.0 ** -24 + 1e-30
-    return a * (share + 2.0 ** -11) + out.abs() * 2.0 ** -8 + 1e-30
+    return a * (share + 2.0 ** -11) + out.abs() * 2.0 ** -8 + small * 2.0 ** -33 + 1e-30

@@ -40,8 +40,8 @@ def _check(step, H, G, D, mode, dtype, seed, causal=True, window=0, q_scale=1.0,
     got = _run(step, q, caches, mode, causal=causal, window=window, scale=scale,
                max_q=step.max_q if max_q is None else max_q)
     sc = D ** -0.5 if scale is None else scale
-    out, a, dz = R.attention(q, *caches, step, mode, sc, causal, window)
-    room = R.attention_tolerance(out, a, dz, dtype, D, max(step.lens + [1]))
+    out, *terms = R.attention(q, *caches, step, mode, sc, causal, window)
+    room = R.attention_tolerance(out, terms, dtype, D, max(step.lens + [1]))
     lo, hi = int(step.starts[0]), int(step.starts[-1])
     err = (got.double() - out).abs()[lo:hi]
     bad = (~(err <= room[lo:hi])).nonzero()
@@ -137,8 +137,8 @@ def test_blocks_of_very_different_scales(dtype, D, news):
     ks[ids[3]] = 0.05
     caches = (kraw, ks, vraw, vs)
     got = _run(step, q, caches, mode, max_q=news)
-    out, a, dz = R.attention(q, *caches, step, mode, D ** -0.5)
-    room = R.attention_tolerance(out, a, dz, dtype, D, 640)
+    out, *terms = R.attention(q, *caches, step, mode, D ** -0.5)
+    room = R.attention_tolerance(out, terms, dtype, D, 640)
     err = (got.double() - out).abs()
     assert bool((err <= room).all()), float((err / room).max())
 
@@ -186,8 +186,8 @@ def test_pages_out_of_range_are_not_seen(dtype, D, news):
         step.pages[0, 2] = bad
         got = _run(step, q, caches, mode, max_q=news, expect_flags=R.PAGE_FLAG)
         step.pages = good
-        out, a, dz = R.attention(q, *caches, step, mode, D ** -0.5, drop=lambda s, j: s == 0 and j // 32 == 2)
-        room = R.attention_tolerance(out, a, dz, dtype, D, 200)
+        out, *terms = R.attention(q, *caches, step, mode, D ** -0.5, drop=lambda s, j: s == 0 and j // 32 == 2)
+        room = R.attention_tolerance(out, terms, dtype, D, 200)
         assert bool(((got.double() - out).abs() <= room).all())
     for starts in ([0, 70, 60], [-3, 40, 60], [50, 10, 60], [0, 2 ** 31 - 1, -2 ** 31]):
         other = R.Step([200, 100], [news, 1], 32, seed=7)
@@ -251,8 +251,8 @@ def test_capture_and_replay_with_new_lengths(news):
         graph.replay()
         torch.cuda.synchronize()
         step.lens = lens
-        want, a, dz = R.attention(q, *caches, step, mode, D ** -0.5)
-        room = R.attention_tolerance(want, a, dz, BF16, D, 1500)
+        want, *terms = R.attention(q, *caches, step, mode, D ** -0.5)
+        room = R.attention_tolerance(want, terms, BF16, D, 1500)
         assert bool(((out.cpu().double() - want).abs() <= room).all()), lens
     assert nvq.nv_pipeline_error() == 0
     del graph
@@ -274,8 +274,8 @@ def test_offsets_past_32_bits(news, D):
     scales[step.pages[0].long().cuda()] = sc.cuda()
     q = torch.randn(news, H * G, D, generator=torch.Generator().manual_seed(1)).to(BF16)
     got = nvq.nv_kv_attention(q.cuda(), codes, scales, codes, scales, *step.dev(), max_q=news).cpu()
-    out, a, dz = R.attention(q, raw, sc, raw, sc, small, "int8", D ** -0.5)
-    assert bool(((got.double() - out).abs() <= R.attention_tolerance(out, a, dz, BF16, D, 300)).all())
+    out, *terms = R.attention(q, raw, sc, raw, sc, small, "int8", D ** -0.5)
+    assert bool(((got.double() - out).abs() <= R.attention_tolerance(out, terms, BF16, D, 300)).all())
 
 
 def test_refusals():
