@@ -481,26 +481,19 @@ def nv_qmm_fp(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, mode: 
     return y
 
 
-class _On:
-    """Makes the tensors' device current for a call, where it is not already, and
-    gives the stream the call goes to: the given one, else that device's current one."""
+# The current stream's handle without building a Stream object around it (4 us a call
+# where the calls below take 10 in all).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
-    __slots__ = ("guard", "stream")
 
-    def __init__(self, device: torch.device, stream):
-        self.guard = None
-        if device.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(device)
-        self.stream = stream
-
-    def __enter__(self) -> int:
-        if self.guard is not None:
-            self.guard.__enter__()
-        return _stream(self.stream)
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _call(fn, index: int, stream, *args) -> int:
+    """fn(*args, stream) on device `index`, made current for the call where it is
+    not; stream None is that device's current stream."""
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            return fn(*args, _raw_stream(index) if stream is None else _stream(stream))
+    return fn(*args, _raw_stream(index) if stream is None else _stream(stream))
 
 
 def nv_moe_route(logits: torch.Tensor, topk: int, score: str = "softmax",
@@ -515,69 +508,66 @@ def nv_moe_route(logits: torch.Tensor, topk: int, score: str = "softmax",
     if logits.dim() != 2 or score not in _ROUTE_SCORES:
         raise ValueError(f"logits must be [T, E] and score one of {sorted(_ROUTE_SCORES)}")
     T, E = logits.shape
-    device = logits.device
-    if bias is not None:
-        _dev(bias, "bias")
-        if bias.dtype != torch.float32 or bias.numel() != E or bias.device != device:
-            raise ValueError("bias must be fp32 [E] on the logits' device")
-    outs = []
-    for t, dtype, name in ((ids, torch.int32, "ids"), (weights, torch.float32, "weights")):
-        if t is None:
-            t = torch.empty(T, max(topk, 0), dtype=dtype, device=device)
-        else:
-            _dev(t, name)
-            if tuple(t.shape) != (T, topk) or t.dtype != dtype or t.device != device:
-                raise ValueError(f"{name} must be {dtype} [T, topk] on the logits' device")
-        outs.append(t)
-    with _On(device, stream) as s:
-        st = lib().nv_moe_route(logits.data_ptr(), _DT.get(logits.dtype, -1), T, E, _ptr(bias),
-                                _ROUTE_SCORES[score], groups, groups if topk_groups is None else topk_groups,
-                                group_top, topk, int(renormalize), scale, outs[0].data_ptr(),
-                                outs[1].data_ptr(), s)
+    device, index = logits.device, logits.get_device()
+    if bias is not None and (bias.get_device() != index or bias.dtype != torch.float32 or
+                             bias.numel() != E or not bias.is_contiguous()):
+        raise ValueError("bias must be contiguous fp32 [E] on the logits' device")
+    if ids is None:
+        ids = torch.empty((T, max(topk, 0)), dtype=torch.int32, device=device)
+    elif tuple(ids.shape) != (T, topk) or ids.dtype != torch.int32 or ids.get_device() != index or \
+            not ids.is_contiguous():
+        raise ValueError("ids must be contiguous int32 [T, topk] on the logits' device")
+    if weights is None:
+        weights = torch.empty((T, max(topk, 0)), dtype=torch.float32, device=device)
+    elif tuple(weights.shape) != (T, topk) or weights.dtype != torch.float32 or \
+            weights.get_device() != index or not weights.is_contiguous():
+        raise ValueError("weights must be contiguous fp32 [T, topk] on the logits' device")
+    st = _call(lib().nv_moe_route, index, stream, logits.data_ptr(), _DT.get(logits.dtype, -1), T, E,
+               None if bias is None else bias.data_ptr(), _ROUTE_SCORES[score], groups,
+               groups if topk_groups is None else topk_groups, group_top, topk, int(renormalize), scale,
+               ids.data_ptr(), weights.data_ptr())
     _check("nv_moe_route", st)
-    return outs[0], outs[1]
+    return ids, weights
 
 
 def _kv_args(k_codes, k_scales, v_codes, v_scales, pages, starts, lens, flags):
     """The cache's and the step descriptor's arguments as the C calls take them,
-    after the checks that need shapes: (cache, steps, flags pointer, H, D, device)."""
-    device = k_codes.device
-    for t, n in ((k_codes, "k_codes"), (k_scales, "k_scales"), (v_codes, "v_codes"),
-                 (v_scales, "v_scales"), (pages, "pages"), (starts, "starts"), (lens, "lens")):
-        if not t.is_cuda or not t.is_contiguous() or t.device != device:
-            raise ValueError(f"{n} must be a contiguous CUDA tensor on the cache's device")
-    if k_codes.dim() != 4 or k_codes.shape != v_codes.shape or k_codes.dtype != v_codes.dtype:
-        raise ValueError("k_codes and v_codes must be [P, H, block, D] alike")
-    P, H, block, D = k_codes.shape
-    mode = _KV_MODES.get(k_codes.dtype)
-    if mode is None:
-        raise ValueError("codes must be torch.int8 or torch.float8_e4m3fn")
-    for t, n in ((k_scales, "k_scales"), (v_scales, "v_scales")):
-        if t.dtype != torch.float32 or t.dim() != 2 or t.shape[0] != P or t.shape[1] != H:
-            raise ValueError(f"{n} must be fp32 [P, H]")
-    S = lens.shape[0] if lens.dim() == 1 else -1
-    if pages.dim() != 2 or pages.shape[0] != S or starts.dim() != 1 or starts.shape[0] != S + 1:
+    after the checks that need shapes: (cache, steps, flags pointer, device index)."""
+    index = k_codes.get_device()
+    for t in (k_codes, k_scales, v_codes, v_scales, pages, starts, lens):
+        if t.get_device() != index or not t.is_contiguous():
+            index = -1
+    if index < 0:
+        raise ValueError("the cache, pages, starts and lens must be contiguous CUDA tensors on one device")
+    shape, dtype = k_codes.shape, k_codes.dtype
+    mode = _KV_MODES.get(dtype)
+    if len(shape) != 4 or shape != v_codes.shape or dtype != v_codes.dtype or mode is None:
+        raise ValueError("k_codes and v_codes must be int8 or float8_e4m3fn [P, H, block, D] alike")
+    if k_scales.shape != shape[:2] or v_scales.shape != shape[:2] or \
+            not (k_scales.dtype == v_scales.dtype == torch.float32):
+        raise ValueError("k_scales and v_scales must be fp32 [P, H]")
+    table = pages.shape
+    S = table[0]
+    if len(table) != 2 or starts.shape != (S + 1,) or lens.shape != (S,):
         raise ValueError("pages [S, max_pages], starts [S + 1] and lens [S] expected")
-    if pages.dtype != torch.int32 or starts.dtype != torch.int32 or lens.dtype != torch.int32:
+    if not (pages.dtype == starts.dtype == lens.dtype == torch.int32):
         raise ValueError("pages, starts and lens must be int32")
-    if flags is not None and (not flags.is_cuda or flags.dtype != torch.int32 or flags.numel() < 1 or
-                              flags.device != device):
-        raise ValueError("flags must be an int32 CUDA tensor on the cache's device")
-    return ((k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), mode, P,
-             H, block, D),
-            (pages.data_ptr(), pages.shape[1], starts.data_ptr(), lens.data_ptr(), S), _ptr(flags), H, D,
-            device)
+    if flags is not None:
+        if flags.get_device() != index or flags.dtype != torch.int32 or flags.numel() < 1:
+            raise ValueError("flags must be an int32 CUDA tensor on the cache's device")
+        flags = flags.data_ptr()
+    return ((k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), mode, *shape),
+            (pages.data_ptr(), table[1], starts.data_ptr(), lens.data_ptr(), S), flags, index)
 
 
-def _kv_rows(t: torch.Tensor, name: str, heads: int, D: int, device) -> int:
+def _kv_rows(t: torch.Tensor, name: str, heads: int, D: int, index: int) -> int:
     """Row stride of a step's tensor [rows, heads, D]: dense heads, any distance between rows."""
-    if not t.is_cuda or t.device != device or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != D:
+    if t.get_device() != index or t.dim() != 3 or t.shape[1:] != (heads, D):
         raise ValueError(f"{name} must be [rows, {heads}, {D}] on the cache's device")
-    rows, dense = t.shape[0], heads * D
     row, head, last = t.stride()
     if (last != 1 and D > 1) or (head != D and heads > 1):
         raise ValueError(f"the heads of a row of {name} must be dense")
-    return row if rows > 1 else dense
+    return row if t.shape[0] > 1 else heads * D
 
 
 def nv_kv_quantize(k: torch.Tensor, v: torch.Tensor, k_codes: torch.Tensor, k_scales: torch.Tensor,
@@ -588,13 +578,13 @@ def nv_kv_quantize(k: torch.Tensor, v: torch.Tensor, k_codes: torch.Tensor, k_sc
     paged 8-bit cache: codes int8 or float8_e4m3fn [P, H, block, D], scales fp32
     [P, H]. Rows starts[s] .. starts[s + 1] are the last tokens of sequence s,
     lens[s] its length with them, pages[s, j] the page of its j-th block."""
-    cache, steps, fl, H, D, device = _kv_args(k_codes, k_scales, v_codes, v_scales, pages, starts, lens, flags)
-    ks, vs = _kv_rows(k, "k", H, D, device), _kv_rows(v, "v", H, D, device)
+    cache, steps, fl, index = _kv_args(k_codes, k_scales, v_codes, v_scales, pages, starts, lens, flags)
+    H, D = cache[6], cache[8]
+    ks, vs = _kv_rows(k, "k", H, D, index), _kv_rows(v, "v", H, D, index)
     if k.shape != v.shape or k.dtype != v.dtype:
         raise ValueError("k and v must be alike")
-    with _On(device, stream) as s:
-        st = lib().nv_kv_quantize(k.data_ptr(), v.data_ptr(), ks, vs, _DT.get(k.dtype, -1), k.shape[0],
-                                  *cache, *steps, fl, s)
+    st = _call(lib().nv_kv_quantize, index, stream, k.data_ptr(), v.data_ptr(), ks, vs,
+               _DT.get(k.dtype, -1), k.shape[0], *cache, *steps, fl)
     _check("nv_kv_quantize", st)
 
 
@@ -605,18 +595,18 @@ def nv_kv_dequantize(k_codes: torch.Tensor, k_scales: torch.Tensor, v_codes: tor
     """(k, v) [rows, H, D]: the last starts[s + 1] - starts[s] tokens of every
     sequence, read back (all of them where starts is the running sum of lens).
     out: a pair of tensors to write to; rows of no sequence are left as they were."""
-    cache, steps, fl, H, D, device = _kv_args(k_codes, k_scales, v_codes, v_scales, pages, starts, lens, flags)
+    cache, steps, fl, index = _kv_args(k_codes, k_scales, v_codes, v_scales, pages, starts, lens, flags)
+    shape = (rows, cache[6], cache[8])
     if out is None:
-        k = torch.empty(rows, H, D, dtype=dtype, device=device)
-        v = torch.empty(rows, H, D, dtype=dtype, device=device)
+        device = k_codes.device
+        k, v = torch.empty(shape, dtype=dtype, device=device), torch.empty(shape, dtype=dtype, device=device)
     else:
         k, v = out
-        for t, n in ((k, "out[0]"), (v, "out[1]")):
-            _dev(t, n)
-            if tuple(t.shape) != (rows, H, D) or t.dtype != dtype or t.device != device:
-                raise ValueError(f"{n} must be {dtype} [rows, H, D] on the cache's device")
-    with _On(device, stream) as s:
-        st = lib().nv_kv_dequantize(*cache, *steps, _DT.get(dtype, -1), rows, k.data_ptr(), v.data_ptr(), fl, s)
+        for t in out:
+            if t.shape != shape or t.dtype != dtype or t.get_device() != index or not t.is_contiguous():
+                raise ValueError(f"out must be two contiguous {dtype} {shape} tensors on the cache's device")
+    st = _call(lib().nv_kv_dequantize, index, stream, *cache, *steps, _DT.get(dtype, -1), rows,
+               k.data_ptr(), v.data_ptr(), fl)
     _check("nv_kv_dequantize", st)
     return k, v
 
@@ -638,29 +628,29 @@ def nv_kv_attention(q: torch.Tensor, k_codes: torch.Tensor, k_scales: torch.Tens
     defaults to D ** -0.5; window > 0 limits a causal row to its last `window`
     tokens; max_q is the largest number of rows of one sequence, if known.
     Returns out [rows, Hq, D]; rows of no sequence are left as they were."""
-    cache, steps, fl, H, D, device = _kv_args(k_codes, k_scales, v_codes, v_scales, pages, starts, lens, flags)
+    cache, steps, fl, index = _kv_args(k_codes, k_scales, v_codes, v_scales, pages, starts, lens, flags)
+    if index != torch.cuda.current_device():  # the workspace's size goes by that device too
+        with torch.cuda.device(index):
+            return nv_kv_attention(q, k_codes, k_scales, v_codes, v_scales, pages, starts, lens, scale, causal,
+                                   window, max_q, workspace, out, flags, stream)
+    H, block, D = cache[6:]
     if q.dim() != 3:
         raise ValueError("q must be [rows, Hq, D]")
-    rows, Hq = q.shape[0], q.shape[1]
-    qs = _kv_rows(q, "q", Hq, D, device)
+    rows, Hq = q.shape[:2]
+    qs = _kv_rows(q, "q", Hq, D, index)
     if out is None:
-        out = torch.empty(rows, Hq, D, dtype=q.dtype, device=device)
-    else:
-        _dev(out, "out")
-        if out.shape != q.shape or out.dtype != q.dtype or out.device != device:
-            raise ValueError("out must be dense and like q")
+        out = torch.empty((rows, Hq, D), dtype=q.dtype, device=q.device)
+    elif out.shape != q.shape or out.dtype != q.dtype or out.get_device() != index or not out.is_contiguous():
+        raise ValueError("out must be contiguous and like q")
     L, dt = lib(), _DT.get(q.dtype, -1)
     if workspace is None:
-        need = L.nv_kv_attention_workspace_size(dt, rows, Hq, H, cache[7], D, steps[1], steps[4], max_q)
+        need = L.nv_kv_attention_workspace_size(dt, rows, Hq, H, block, D, steps[1], steps[4], max_q)
         if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    else:
-        _dev(workspace, "workspace")
-    wp, wb = (None, 0) if workspace is None else (workspace.data_ptr(),
-                                                  workspace.numel() * workspace.element_size())
-    with _On(device, stream) as s:
-        st = L.nv_kv_attention(q.data_ptr(), qs, dt, rows, Hq, *cache, *steps,
-                               D ** -0.5 if scale is None else scale, int(causal), window, max_q, wp, wb,
-                               out.data_ptr(), fl, s)
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor on the cache's device")
+    wp, wb = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
+    st = _call(L.nv_kv_attention, index, stream, q.data_ptr(), qs, dt, rows, Hq, *cache, *steps,
+               D ** -0.5 if scale is None else scale, int(causal), window, max_q, wp, wb, out.data_ptr(), fl)
     _check("nv_kv_attention", st)
     return out

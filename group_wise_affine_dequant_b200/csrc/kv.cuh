@@ -79,12 +79,15 @@ __host__ __device__ inline int64_t kv_items(int64_t rows, int S, int64_t mul, in
 __device__ __forceinline__ int64_t kv_first_item(const KvSteps& st, int s, int64_t mul, int64_t per, int extra) {
     return clamped_start(st, s) * mul / per + static_cast<int64_t>(s) * extra;
 }
-// The last sequence whose items start at or before `item` (by one warp: 32
-// probes a step, so one step up to 32 sequences and two up to 1024).
+// The last sequence whose items start at or before `item`, by one warp: the starts
+// ascend, so it is their count. Up to kProbe starts a lane are read at once (256
+// sequences in one round trip to memory); more sequences are narrowed first,
+// 32 probes a step. The lengths' lines are touched beside them for seq_span.
+constexpr int kProbe = 8;
 __device__ __forceinline__ int kv_find_seq(const KvSteps& st, int64_t item, int64_t mul, int64_t per, int extra) {
     const int lane = threadIdx.x & 31;
     int lo = 0, hi = st.S;
-    while (hi - lo > 1) {
+    while (hi - lo > 32 * kProbe) {
         const int step = (hi - lo + 31) / 32;
         const int p = lo + lane * step;
         const bool at_or_before = p < hi && kv_first_item(st, p, mul, per, extra) <= item;
@@ -92,7 +95,17 @@ __device__ __forceinline__ int kv_find_seq(const KvSteps& st, int64_t item, int6
         lo += (n > 0 ? n - 1 : 0) * step;
         hi = hi < lo + step ? hi : lo + step;
     }
-    return lo;
+    int before = 0;
+#pragma unroll
+    for (int i = 0; i < kProbe; ++i) {
+        const int p = lo + i * 32 + lane;
+        if (lo + i * 32 < hi && p < hi) {
+            before += kv_first_item(st, p, mul, per, extra) <= item;
+            asm volatile("{\n\t.reg .b32 unused;\n\tld.global.nc.b32 unused, [%0];\n\t}" ::"l"(st.lens + p));
+        }
+    }
+    before = __reduce_add_sync(0xffffffffu, before);
+    return before > 0 ? lo + before - 1 : lo;
 }
 
 constexpr float kInt8Max = 127.f;

@@ -530,14 +530,16 @@ kv_attn_decode_kernel(const __grid_constant__ DecodeArgs p, const __grid_constan
 }
 
 // Join the chunks of the rows whose sequence took several: one CTA per row of
-// partials, warp w sums chunks w, w + 4, ... in order, then the four sums.
+// partials, of one warp per eight chunks there can be; warp w sums chunks w, w + warps,
+// ... in order (its loads all in flight), then the warps' sums are added in order.
+constexpr int kJoinWarps = 16;
 template <int D>
-__global__ void __launch_bounds__(128) kv_attn_join_kernel(const __grid_constant__ DecodeArgs p) {
-    __shared__ float sums[4][D];
-    __shared__ float weights[4];
+__global__ void __launch_bounds__(32 * kJoinWarps) kv_attn_join_kernel(const __grid_constant__ DecodeArgs p) {
+    __shared__ float sums[kJoinWarps][D];
+    __shared__ float weights[kJoinWarps];
     pdl_launch_dependents();
     pdl_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int G = p.a.Hq / p.c.H;
     int64_t t;
     int s, hq;
@@ -563,8 +565,8 @@ __global__ void __launch_bounds__(128) kv_attn_join_kernel(const __grid_constant
     constexpr int V = D / 32;  // values a lane
     float acc[V] = {};
     float weight = 0.f;
-#pragma unroll 4
-    for (int k = warp; k < w.chunks; k += 4) {
+#pragma unroll 8
+    for (int k = warp; k < w.chunks; k += warps) {
         const float e = exp2f(__ldcg(p.part_lse + at + k) - top);
         weight += e;
 #pragma unroll
@@ -578,11 +580,14 @@ __global__ void __launch_bounds__(128) kv_attn_join_kernel(const __grid_constant
     for (int i = 0; i < V; ++i) sums[warp][lane * V + i] = acc[i];
     if (lane == 0) weights[warp] = weight;
     __syncthreads();
-    const float all = (weights[0] + weights[1]) + (weights[2] + weights[3]);
-    const float inv = all > 0.f ? 1.f / all : 0.f;
-    for (int d = threadIdx.x; d < D; d += 128)
-        static_cast<uint16_t*>(p.a.out)[(t * p.a.Hq + hq) * D + d] =
-            f32_to_bf16_bits(((sums[0][d] + sums[1][d]) + (sums[2][d] + sums[3][d])) * inv);
+    for (int d = threadIdx.x; d < D; d += blockDim.x) {
+        float all = 0.f, x = 0.f;
+        for (int i = 0; i < warps; ++i) {
+            all += weights[i];
+            x += sums[i][d];
+        }
+        static_cast<uint16_t*>(p.a.out)[(t * p.a.Hq + hq) * D + d] = f32_to_bf16_bits(all > 0.f ? x / all : 0.f);
+    }
 }
 
 // K or V codes as [P * H][block][D] bytes, boxes of min(block, 64) tokens.
@@ -621,7 +626,8 @@ cudaError_t launch(const DecodeArgs& p, int64_t part_rows, cudaStream_t stream, 
     e = cudaLaunchKernelEx(&cfg, kv_attn_decode_kernel<MODE, D>, p, kmap, vmap);
     if (e != cudaSuccess || p.max_chunks <= 1) return e;
     cfg.gridDim = dim3(static_cast<unsigned>(part_rows), 1, 1);
-    cfg.blockDim = dim3(128, 1, 1);
+    const int warps = (p.max_chunks + 7) / 8;
+    cfg.blockDim = dim3(32 * (warps < kJoinWarps ? warps : kJoinWarps), 1, 1);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, kv_attn_join_kernel<D>, p);
 }

@@ -8,10 +8,11 @@
 // larger one; then the codes already there are read, scaled by old / new and
 // rounded again through a 256-entry table (a code has only 256 values).
 //
-// Write: one CTA per (block of tokens, head, K or V) holds the block's new
-// values in registers (64 per thread), so they are read once: maximum, scale,
-// codes. Read back: one CTA per block of tokens and head. Both are bound by
-// memory: 2 bytes in and 1 out per bf16 value, and the reverse.
+// Both kernels: one CTA per block of tokens and run of planes (a plane is K or V of
+// one head). Writing, a plane's new values stay in registers between the maximum
+// and the codes, so they are read once; a few tokens (a decoding step) take one
+// warp a plane, whole blocks the CTA. Bound by memory: 2 bytes in and 1 out per
+// bf16 value, and the reverse for the read-back.
 #include <cstdint>
 
 #include "kv.cuh"
@@ -20,32 +21,53 @@
 namespace nvq {
 namespace {
 
-constexpr int kChunks = 8;  // 8-value chunks per thread
-constexpr int kMaxThreads = 512;  // block 128 x D 256: 64 values per thread
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kKeep = 4;  // 8-value chunks a thread keeps: a block of 64 tokens of 128 values
 
-struct Values8 {
-    float v[8];
-};
-
+// Eight values as they are stored.
 template <int DT>
-__device__ __forceinline__ Values8 load8(const void* p, int64_t i) {
-    Values8 r;
-    if constexpr (DT == NV_F32) {
-        const float4 a = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + i));
-        const float4 b = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + i) + 1);
-        r.v[0] = a.x; r.v[1] = a.y; r.v[2] = a.z; r.v[3] = a.w;
-        r.v[4] = b.x; r.v[5] = b.y; r.v[6] = b.z; r.v[7] = b.w;
-    } else {
-        const uint4 a = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i));
-        const uint32_t u[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            r.v[2 * j] = __uint_as_float(u[j] << 16);
-            r.v[2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
-        }
+struct Raw8;
+template <>
+struct Raw8<NV_BF16> {
+    uint4 u;
+    __device__ __forceinline__ void load(const void* p, int64_t i) {
+        u = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i));
     }
-    return r;
-}
+    __device__ __forceinline__ void clear() { u = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ float get(int j) const {
+        const uint32_t w = j < 2 ? u.x : j < 4 ? u.y : j < 6 ? u.z : u.w;
+        return __uint_as_float(j & 1 ? w & 0xFFFF0000u : w << 16);
+    }
+    // largest magnitude's bits as fp32 bits (NaN and infinity above every number)
+    __device__ __forceinline__ uint32_t most() const {
+        const uint32_t m = __vmaxu2(__vmaxu2(u.x & 0x7FFF7FFFu, u.y & 0x7FFF7FFFu),
+                                    __vmaxu2(u.z & 0x7FFF7FFFu, u.w & 0x7FFF7FFFu));
+        return max(m << 16, m & 0xFFFF0000u);
+    }
+};
+template <>
+struct Raw8<NV_F32> {
+    uint4 u[2];
+    __device__ __forceinline__ void load(const void* p, int64_t i) {
+        const uint4* q = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + i);
+        u[0] = __ldg(q);
+        u[1] = __ldg(q + 1);
+    }
+    __device__ __forceinline__ void clear() { u[0] = u[1] = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ float get(int j) const {
+        const uint4& w = u[j >> 2];
+        const int k = j & 3;
+        return __uint_as_float(k == 0 ? w.x : k == 1 ? w.y : k == 2 ? w.z : w.w);
+    }
+    __device__ __forceinline__ uint32_t most() const {
+        uint32_t m = 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            m = max(m, max(max(u[h].x & 0x7FFFFFFFu, u[h].y & 0x7FFFFFFFu), max(u[h].z & 0x7FFFFFFFu, u[h].w & 0x7FFFFFFFu)));
+        return m;
+    }
+};
 
 // The integer nearest to x / s (ties to even), |x / s| <= 127.5: a first guess
 // by the reciprocal is off by at most one, and the remainder x - c s is exact
@@ -78,19 +100,19 @@ __device__ __forceinline__ float e4m3_quotient(float x, float s) {
 }
 
 template <int MODE>
-__device__ __forceinline__ uint2 encode8(const Values8& x, float s, float inv) {
+__device__ __forceinline__ uint2 encode8(const float (&x)[8], float s, float inv) {
     uint32_t w[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         if constexpr (MODE == NV_KV_INT8) {
             uint32_t b[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) b[j] = int8_code(x.v[4 * h + j], s, inv);
+            for (int j = 0; j < 4; ++j) b[j] = int8_code(x[4 * h + j], s, inv);
             w[h] = b[0] | (b[1] << 8) | (b[2] << 16) | (b[3] << 24);
         } else {
             float q[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) q[j] = e4m3_quotient(x.v[4 * h + j], s);
+            for (int j = 0; j < 4; ++j) q[j] = e4m3_quotient(x[4 * h + j], s);
             const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(q[0], q[1]), __NV_SATFINITE, __NV_E4M3);
             const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(q[2], q[3]), __NV_SATFINITE, __NV_E4M3);
             w[h] = lo | (hi << 16);
@@ -115,184 +137,257 @@ __device__ __forceinline__ uint8_t recode(uint32_t byte, float old_scale, float 
     }
 }
 
-// Largest of one unsigned value per thread, over the CTA; every thread gets it.
-__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* warp_max) {
-    v = __reduce_max_sync(0xffffffffu, v);
-    if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = v;
-    __syncthreads();
-    const int warps = blockDim.x >> 5;
-    uint32_t r = 0;
-    for (int i = 0; i < warps; ++i) r = max(r, warp_max[i]);
-    return r;
+// The block of tokens a CTA works on: sequence, page and this step's slots in it.
+struct BlockWork {
+    int page;          // -1: out of range (flagged) or nothing to do
+    int slot0, slot1;  // the step's tokens in the block
+    int64_t row0;      // row of slot0
+    bool any;          // the block has tokens of the step
+};
+__device__ __forceinline__ BlockWork block_work(const KvCache& c, const KvSteps& st, const SeqSpan& span, int s,
+                                                int64_t j) {
+    BlockWork w{};
+    w.page = -1;
+    const int first = span.first < 0 ? 0 : span.first;
+    const int64_t b = first / c.block + j;
+    if (j < 0 || span.n == 0 || b * c.block >= span.len) return w;
+    const int base = static_cast<int>(b * c.block);
+    w.any = true;
+    w.slot0 = first > base ? first - base : 0;
+    w.slot1 = span.len - base < c.block ? span.len - base : c.block;
+    w.row0 = span.row0 + (base + w.slot0 - span.first);
+    w.page = page_of(st, c, s, static_cast<int>(b));
+    return w;
 }
 
 struct QuantArgs {
     const void* x[2];  // k, v
     int64_t stride[2];
+    int planes;        // planes a CTA takes
     KvCache c;
     KvSteps st;
 };
 
-template <int DT, int MODE>
-__global__ void __launch_bounds__(kMaxThreads) kv_quantize_kernel(const __grid_constant__ QuantArgs a) {
-    __shared__ uint32_t warp_max[kMaxThreads / 32];
-    __shared__ uint8_t table[256];
+// One plane of a block by a team of threads (a warp or the CTA); `most` finds the
+// team's maximum and is a barrier for it.
+template <int DT, int MODE, class Most, class Sync>
+__device__ __forceinline__ void quantize_plane(const QuantArgs& a, const BlockWork& w, int plane, int rank, int size,
+                                               uint8_t* table, const Most& team_most, const Sync& sync) {
     const KvCache& c = a.c;
-    pdl_launch_dependents();
-    pdl_wait();
-    const int which = blockIdx.y & 1, h = blockIdx.y >> 1;
-    const int s = kv_find_seq(a.st, blockIdx.x, 1, c.block, 2);
-    const SeqSpan span = seq_span(a.st, s, c.block);
-    const int first = span.first < 0 ? 0 : span.first;
-    const int64_t j = static_cast<int64_t>(blockIdx.x) - kv_first_item(a.st, s, 1, c.block, 2);
-    const int64_t b = first / c.block + j;
-    if (j < 0 || span.n == 0 || b * c.block >= span.len) return;
-    const int page = page_of(a.st, c, s, static_cast<int>(b));
-    if (page < 0) return;
-    // this block's new tokens: slots slot0 .. slot1, rows from row0 on
-    const int base = static_cast<int>(b * c.block);
-    const int slot0 = first > base ? first - base : 0;
-    const int slot1 = span.len - base < c.block ? span.len - base : c.block;
-    const int64_t row0 = span.row0 + (base + slot0 - span.first);
+    const int which = plane & 1, h = plane >> 1;
     const int vecs = c.D / 8;
-    const int chunks = (slot1 - slot0) * vecs;
-    const void* x = a.x[which];
-    const int64_t stride = a.stride[which];
-    uint8_t* codes = (which ? c.v_codes : c.k_codes) +
-                     (static_cast<int64_t>(page) * c.H + h) * (static_cast<int64_t>(c.block) * c.D);
-    float* scale_at = (which ? c.v_scales : c.k_scales) + static_cast<int64_t>(page) * c.H + h;
-    const float old = slot0 > 0 ? *scale_at : 0.f;
-
-    Values8 val[kChunks];
-    uint32_t most = 0;  // largest finite magnitude, as bits; bit 31: something is not finite
+    const int chunks = (w.slot1 - w.slot0) * vecs;
+    const void* x = which ? a.x[1] : a.x[0];
+    const int64_t stride = which ? a.stride[1] : a.stride[0];
+    const int64_t at = static_cast<int64_t>(w.page) * c.H + h;
+    uint8_t* codes = (which ? c.v_codes : c.k_codes) + at * (static_cast<int64_t>(c.block) * c.D);
+    float* scale_at = (which ? c.v_scales : c.k_scales) + at;
+    const int64_t x0 = w.row0 * stride + static_cast<int64_t>(h) * c.D;
+    auto place = [&](int i) {  // chunk i's first value
+        const int tok = i / vecs;
+        return x0 + tok * stride + (i - tok * vecs) * 8;
+    };
+    Raw8<DT> keep[kKeep];
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i) {
-        const int at = threadIdx.x + i * blockDim.x;
-        if (at >= chunks) break;
-        const int tok = at / vecs, d = (at - tok * vecs) * 8;
-        val[i] = load8<DT>(x, (row0 + tok) * stride + static_cast<int64_t>(h) * c.D + d);
+    for (int k = 0; k < kKeep; ++k) {
+        keep[k].clear();
+        if (rank + k * size < chunks) keep[k].load(x, place(rank + k * size));
     }
-    uint32_t odd = 0;
+    const float old = w.slot0 > 0 ? *scale_at : 0.f;
+    uint32_t most = 0;
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i) {
-        if (threadIdx.x + i * blockDim.x >= chunks) break;
+    for (int k = 0; k < kKeep; ++k) most = max(most, keep[k].most());
+    for (int i = rank + kKeep * size; i < chunks; i += size) {
+        Raw8<DT> r;
+        r.load(x, place(i));
+        most = max(most, r.most());
+    }
+    most = team_most(most);
+    const bool odd = most >= 0x7F800000u;  // NaN or infinities among the values: the maximum of the others
+    if (odd) {
+        most = 0;
+        for (int i = rank; i < chunks; i += size) {
+            Raw8<DT> r;
+            r.load(x, place(i));
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t u = __float_as_uint(val[i].v[j]) & 0x7FFFFFFFu;
-            if (u < 0x7F800000u)
-                most = max(most, u);
-            else
-                odd = 1;
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t u = __float_as_uint(r.get(j)) & 0x7FFFFFFFu;
+                if (u < 0x7F800000u) most = max(most, u);
+            }
         }
+        sync();
+        most = team_most(most);
     }
-    most = block_max(most, warp_max);
-    const bool any_odd = __syncthreads_or(odd);
     constexpr float kLargest = MODE == NV_KV_INT8 ? kInt8Max : kE4m3Max;
     const float scale = fmaxf(old, __fdiv_rn(__uint_as_float(most), kLargest));
-    if (threadIdx.x == 0) *scale_at = scale;
+    if (rank == 0) *scale_at = scale;
 
-    if (slot0 > 0 && scale > old) {  // the same for the whole CTA
-        for (int i = threadIdx.x; i < 256; i += blockDim.x) table[i] = recode<MODE>(i, old, scale);
-        __syncthreads();
-        uint32_t* words = reinterpret_cast<uint32_t*>(codes);
-        for (int i = threadIdx.x; i < slot0 * c.D / 4; i += blockDim.x) {
-            const uint32_t w = words[i];
-            words[i] = table[w & 255u] | (table[w >> 8 & 255u] << 8) | (table[w >> 16 & 255u] << 16) |
-                       (static_cast<uint32_t>(table[w >> 24]) << 24);
+    if (w.slot0 > 0 && scale > old) {  // the same for the whole team
+        sync();  // the previous plane's reads of the table
+        for (int i = rank; i < 256; i += size) table[i] = recode<MODE>(i, old, scale);
+        sync();
+        uint4* words = reinterpret_cast<uint4*>(codes);
+        for (int i = rank; i < w.slot0 * c.D / 16; i += size) {
+            uint4 u = words[i];
+            uint32_t v[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                v[k] = table[v[k] & 255u] | (table[v[k] >> 8 & 255u] << 8) | (table[v[k] >> 16 & 255u] << 16) |
+                       (static_cast<uint32_t>(table[v[k] >> 24]) << 24);
+            words[i] = make_uint4(v[0], v[1], v[2], v[3]);
         }
     }
 
     // a tiny scale's reciprocal or remainders would leave the normal range: move both by 2^64, exactly
     const float lift = scale < 8.6736174e-19f ? 18446744073709551616.f : 1.f;  // 2^-60, 2^64
     const float s2 = scale * lift, inv = scale > 0.f ? 1.f / s2 : 0.f;
-#pragma unroll
-    for (int i = 0; i < kChunks; ++i) {
-        const int at = threadIdx.x + i * blockDim.x;
-        if (at >= chunks) break;
-        uint2 w = make_uint2(0u, 0u);
+    auto store = [&](const Raw8<DT>& r, int i) {
+        uint2 o = make_uint2(0u, 0u);
         if (scale > 0.f) {
+            float f[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float f = val[i].v[j];
-                if (any_odd) {  // NaN is kept as 0, an infinity as the largest code
-                    f = f == f ? f : 0.f;
-                    f = fminf(fmaxf(f, -kLargest * scale), kLargest * scale);
+            for (int j = 0; j < 8; ++j) f[j] = r.get(j);
+            if (odd) {  // NaN is kept as 0, an infinity as the largest code
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    f[j] = f[j] == f[j] ? f[j] : 0.f;
+                    f[j] = fminf(fmaxf(f[j], -kLargest * scale), kLargest * scale);
                 }
-                val[i].v[j] = f * lift;
             }
-            w = encode8<MODE>(val[i], s2, inv);
+            if (lift != 1.f) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) f[j] *= lift;
+            }
+            o = encode8<MODE>(f, s2, inv);
         }
-        const int tok = at / vecs, d = (at - tok * vecs) * 8;
-        *reinterpret_cast<uint2*>(codes + static_cast<int64_t>(slot0 + tok) * c.D + d) = w;
+        // the block's new slots follow one another in the page: chunk i of them is 8 bytes on
+        *reinterpret_cast<uint2*>(codes + static_cast<int64_t>(w.slot0) * c.D + 8 * static_cast<int64_t>(i)) = o;
+    };
+#pragma unroll
+    for (int k = 0; k < kKeep; ++k)
+        if (rank + k * size < chunks) store(keep[k], rank + k * size);
+    for (int i = rank + kKeep * size; i < chunks; i += size) {
+        Raw8<DT> r;
+        r.load(x, place(i));
+        store(r, i);
+    }
+}
+
+template <int DT, int MODE>
+__global__ void __launch_bounds__(kThreads, 3) kv_quantize_kernel(const __grid_constant__ QuantArgs a) {
+    __shared__ uint32_t warp_most[2][kWarps];
+    __shared__ uint8_t table[kWarps][256];
+    pdl_launch_dependents();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int s = kv_find_seq(a.st, blockIdx.x, 1, a.c.block, 2);
+    const SeqSpan span = seq_span(a.st, s, a.c.block);
+    const BlockWork w = block_work(a.c, a.st, span, s, static_cast<int64_t>(blockIdx.x) - kv_first_item(a.st, s, 1, a.c.block, 2));
+    if (w.page < 0) return;
+    const int p0 = blockIdx.y * a.planes;
+    const int p1 = p0 + a.planes < 2 * a.c.H ? p0 + a.planes : 2 * a.c.H;
+    if ((w.slot1 - w.slot0) * (a.c.D / 8) <= 32 * kKeep) {
+        for (int p = p0 + warp; p < p1; p += kWarps)
+            quantize_plane<DT, MODE>(a, w, p, lane, 32, table[warp],
+                                     [](uint32_t v) { return __reduce_max_sync(0xffffffffu, v); }, [] { __syncwarp(); });
+    } else {
+        int turn = 0;  // two buffers: one barrier a maximum is enough
+        for (int p = p0; p < p1; ++p) {
+            quantize_plane<DT, MODE>(
+                a, w, p, threadIdx.x, kThreads, table[0],
+                [&](uint32_t v) {
+                    v = __reduce_max_sync(0xffffffffu, v);
+                    turn ^= 1;
+                    if (lane == 0) warp_most[turn][warp] = v;
+                    __syncthreads();
+#pragma unroll
+                    for (int i = 0; i < kWarps; ++i) v = max(v, warp_most[turn][i]);
+                    return v;
+                },
+                [] { __syncthreads(); });
+        }
     }
 }
 
 struct DequantArgs {
     void* out[2];  // k, v [rows, H, D]
+    int planes;
     KvCache c;
     KvSteps st;
 };
 
 template <int DT, int MODE>
-__global__ void __launch_bounds__(256) kv_dequantize_kernel(const __grid_constant__ DequantArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) kv_dequantize_kernel(const __grid_constant__ DequantArgs a) {
     const KvCache& c = a.c;
     pdl_launch_dependents();
     pdl_wait();
-    const int which = blockIdx.y & 1, h = blockIdx.y >> 1;
     const int s = kv_find_seq(a.st, blockIdx.x, 1, c.block, 2);
     const SeqSpan span = seq_span(a.st, s, c.block);
-    // rows in front of the sequence's first token (a bad descriptor) read as zeros, with its first block
-    const int first = span.first < 0 ? 0 : span.first;
     const int64_t j = static_cast<int64_t>(blockIdx.x) - kv_first_item(a.st, s, 1, c.block, 2);
-    const int64_t b = first / c.block + j;
-    if (j < 0) return;
+    const BlockWork w = block_work(c, a.st, span, s, j);
+    const int p0 = blockIdx.y * a.planes;
+    const int count = p0 + a.planes < 2 * c.H ? a.planes : 2 * c.H - p0;
     const int vecs = c.D / 16;
-    auto store = [&](int64_t row, int d, const float* f) {
-        const int64_t at = (row * c.H + h) * c.D + d;
+    auto store = [&](int plane, int64_t row, int d, const float (&f)[16]) {
+        const int64_t at = (row * c.H + (plane >> 1)) * c.D + d;
+        void* out = plane & 1 ? a.out[1] : a.out[0];
         if constexpr (DT == NV_F32) {
-            float4* o = reinterpret_cast<float4*>(static_cast<float*>(a.out[which]) + at);
+            float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
         } else {
-            uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out[which]) + at);
-            uint32_t w[8];
+            uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at);
+            uint32_t v[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(f[2 * i + 1]), "f"(f[2 * i]));
-            o[0] = make_uint4(w[0], w[1], w[2], w[3]);
-            o[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v[i]) : "f"(f[2 * i + 1]), "f"(f[2 * i]));
+            o[0] = make_uint4(v[0], v[1], v[2], v[3]);
+            o[1] = make_uint4(v[4], v[5], v[6], v[7]);
         }
     };
-    float f[16];
-    if (j == 0 && span.first < 0) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) f[i] = 0.f;
+    const float zeros[16] = {};
+    if (j == 0 && span.first < 0) {  // rows in front of the sequence (a bad length): with its first block
         const int64_t missing = span.n < -span.first ? span.n : -span.first;
-        for (int64_t i = threadIdx.x; i < missing * vecs; i += blockDim.x)
-            store(span.row0 + i / vecs, static_cast<int>(i % vecs) * 16, f);
-    }
-    if (span.n == 0 || b * c.block >= span.len) return;
-    const int page = page_of(a.st, c, s, static_cast<int>(b));
-    const int base = static_cast<int>(b * c.block);
-    const int slot0 = first > base ? first - base : 0;
-    const int slot1 = span.len - base < c.block ? span.len - base : c.block;
-    const int64_t row0 = span.row0 + (base + slot0 - span.first);
-    const int chunks = (slot1 - slot0) * vecs;
-    const int64_t block_at = page < 0 ? 0 : static_cast<int64_t>(page) * c.H + h;
-    const uint8_t* codes = (which ? c.v_codes : c.k_codes) + block_at * (static_cast<int64_t>(c.block) * c.D);
-    const float scale = page < 0 ? 0.f : __ldg((which ? c.v_scales : c.k_scales) + block_at);
-    for (int i = threadIdx.x; i < chunks; i += blockDim.x) {
-        const int tok = i / vecs, d = (i - tok * vecs) * 16;
-        if (page < 0) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) f[e] = 0.f;
-        } else {
-            const uint4 w = __ldg(reinterpret_cast<const uint4*>(codes + static_cast<int64_t>(slot0 + tok) * c.D + d));
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int e = 0; e < 16; ++e) f[e] = code_value<MODE>(u[e / 4] >> (8 * (e & 3)) & 255u) * scale;
+        for (int64_t i = threadIdx.x; i < missing * vecs * count; i += kThreads) {
+            const int64_t k = i / vecs;
+            store(p0 + static_cast<int>(k % count), span.row0 + k / count, static_cast<int>(i % vecs) * 16, zeros);
         }
-        store(row0 + tok, d, f);
+    }
+    if (!w.any) return;
+    const int chunks = (w.slot1 - w.slot0) * vecs;
+    if (w.page < 0) {
+        for (int i = threadIdx.x; i < chunks * count; i += kThreads) {
+            const int p = i / chunks, k = i - p * chunks, tok = k / vecs;
+            store(p0 + p, w.row0 + tok, (k - tok * vecs) * 16, zeros);
+        }
+        return;
+    }
+    const int64_t bytes = static_cast<int64_t>(c.block) * c.D;
+    constexpr int kUnroll = 4;
+    for (int i0 = threadIdx.x; i0 < chunks * count; i0 += kThreads * kUnroll) {
+        uint4 u[kUnroll];
+        float scale[kUnroll];
+#pragma unroll
+        for (int n = 0; n < kUnroll; ++n) {
+            const int i = i0 + n * kThreads;
+            if (i >= chunks * count) break;
+            const int p = i / chunks, k = i - p * chunks, plane = p0 + p;
+            const int64_t at = static_cast<int64_t>(w.page) * c.H + (plane >> 1);
+            u[n] = __ldg(reinterpret_cast<const uint4*>((plane & 1 ? c.v_codes : c.k_codes) + at * bytes +
+                                                       static_cast<int64_t>(w.slot0) * c.D + 16 * static_cast<int64_t>(k)));
+            scale[n] = __ldg((plane & 1 ? c.v_scales : c.k_scales) + at);
+        }
+#pragma unroll
+        for (int n = 0; n < kUnroll; ++n) {
+            const int i = i0 + n * kThreads;
+            if (i >= chunks * count) break;
+            const int p = i / chunks, k = i - p * chunks, tok = k / vecs;
+            const uint32_t x[4] = {u[n].x, u[n].y, u[n].z, u[n].w};
+            float f[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) f[e] = code_value<MODE>(x[e / 4] >> (8 * (e & 3)) & 255u) * scale[n];
+            store(p0 + p, w.row0 + tok, (k - tok * vecs) * 16, f);
+        }
     }
 }
 
@@ -310,31 +405,40 @@ cudaError_t launch_pdl(void (*kernel)(Args...), dim3 grid, int threads, cudaStre
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// Planes a CTA takes: as many as leave about six CTAs for every SM, so that few
+// blocks of tokens are spread over their heads and many amortise the lookup.
+int planes_per_cta(const KvCache& c, int64_t items) {
+    const int64_t runs = (6 * 148 + items - 1) / items;
+    const int64_t planes = (2 * c.H + runs - 1) / runs;
+    return static_cast<int>(planes < 1 ? 1 : planes);
+}
+
 }  // namespace
 
 cudaError_t launch_kv_quantize(const void* k, const void* v, int64_t k_stride, int64_t v_stride, int dt,
                                const KvCache& c, const KvSteps& st, cudaStream_t stream) {
-    QuantArgs a{{k, v}, {k_stride, v_stride}, c, st};
-    const int threads = (c.block * c.D / 64 + 31) / 32 * 32;
-    const dim3 grid(static_cast<unsigned>(kv_items(st.rows, st.S, 1, c.block, 2)), 2 * c.H, 1);
+    const int64_t items = kv_items(st.rows, st.S, 1, c.block, 2);
+    const int planes = planes_per_cta(c, items);
+    QuantArgs a{{k, v}, {k_stride, v_stride}, planes, c, st};
+    const dim3 grid(static_cast<unsigned>(items), (2 * c.H + planes - 1) / planes, 1);
     if (dt == NV_F32)
-        return c.mode == NV_KV_INT8 ? launch_pdl(kv_quantize_kernel<NV_F32, NV_KV_INT8>, grid, threads, stream, a)
-                                    : launch_pdl(kv_quantize_kernel<NV_F32, NV_KV_E4M3>, grid, threads, stream, a);
-    return c.mode == NV_KV_INT8 ? launch_pdl(kv_quantize_kernel<NV_BF16, NV_KV_INT8>, grid, threads, stream, a)
-                                : launch_pdl(kv_quantize_kernel<NV_BF16, NV_KV_E4M3>, grid, threads, stream, a);
+        return c.mode == NV_KV_INT8 ? launch_pdl(kv_quantize_kernel<NV_F32, NV_KV_INT8>, grid, kThreads, stream, a)
+                                    : launch_pdl(kv_quantize_kernel<NV_F32, NV_KV_E4M3>, grid, kThreads, stream, a);
+    return c.mode == NV_KV_INT8 ? launch_pdl(kv_quantize_kernel<NV_BF16, NV_KV_INT8>, grid, kThreads, stream, a)
+                                : launch_pdl(kv_quantize_kernel<NV_BF16, NV_KV_E4M3>, grid, kThreads, stream, a);
 }
 
 cudaError_t launch_kv_dequantize(void* k, void* v, int dt, const KvCache& c, const KvSteps& st,
                                  cudaStream_t stream) {
-    DequantArgs a{{k, v}, c, st};
-    int threads = (c.block * c.D / 16 + 31) / 32 * 32;
-    threads = threads < 256 ? threads : 256;
-    const dim3 grid(static_cast<unsigned>(kv_items(st.rows, st.S, 1, c.block, 2)), 2 * c.H, 1);
+    const int64_t items = kv_items(st.rows, st.S, 1, c.block, 2);
+    const int planes = planes_per_cta(c, items);
+    DequantArgs a{{k, v}, planes, c, st};
+    const dim3 grid(static_cast<unsigned>(items), (2 * c.H + planes - 1) / planes, 1);
     if (dt == NV_F32)
-        return c.mode == NV_KV_INT8 ? launch_pdl(kv_dequantize_kernel<NV_F32, NV_KV_INT8>, grid, threads, stream, a)
-                                    : launch_pdl(kv_dequantize_kernel<NV_F32, NV_KV_E4M3>, grid, threads, stream, a);
-    return c.mode == NV_KV_INT8 ? launch_pdl(kv_dequantize_kernel<NV_BF16, NV_KV_INT8>, grid, threads, stream, a)
-                                : launch_pdl(kv_dequantize_kernel<NV_BF16, NV_KV_E4M3>, grid, threads, stream, a);
+        return c.mode == NV_KV_INT8 ? launch_pdl(kv_dequantize_kernel<NV_F32, NV_KV_INT8>, grid, kThreads, stream, a)
+                                    : launch_pdl(kv_dequantize_kernel<NV_F32, NV_KV_E4M3>, grid, kThreads, stream, a);
+    return c.mode == NV_KV_INT8 ? launch_pdl(kv_dequantize_kernel<NV_BF16, NV_KV_INT8>, grid, kThreads, stream, a)
+                                : launch_pdl(kv_dequantize_kernel<NV_BF16, NV_KV_E4M3>, grid, kThreads, stream, a);
 }
 
 }  // namespace nvq

@@ -8,19 +8,21 @@
 //
 // One warp holds one token: lane l keeps experts l * VPL .. l * VPL + VPL - 1
 // in registers, so a group is a run of whole lanes for the usual power-of-two
-// sizes. Bound by the logits' read for many tokens and by latency for few;
-// the selection (topk passes of two warp reductions) is the work in between.
+// sizes. Every expert becomes one 32-bit key: its score's (or logit's) order with
+// the low log2(VPL) bits replaced by its place in the lane. Each lane sorts its keys
+// once; a pass takes the largest head of all lanes (one warp reduction) and moves
+// that lane's keys up. Bound by the logits' read for many tokens (the sort and the
+// passes take about as many issue slots) and by latency for few.
 //
-// Who is chosen is exact: scores that differ only beyond fp32 are not left
-// to fp32's rounding.
+// Who is chosen is exact: scores that differ only beyond fp32, or in the bits that a
+// key lacks, are not left to rounding.
 //   * Without a bias both score functions grow with z, so experts (and groups
-//     ranked by one score) are compared by z itself, which is exact.
+//     ranked by one score) are compared by z itself; a bf16 z keeps all its bits.
 //   * With a bias, or where a group's score is a sum of two, comparisons run in
-//     fp32 and every one that decides (neighbours in the chosen order, the last
+//     fp32, and every one that decides (neighbours in the chosen order, the last
 //     chosen and the best refused, the groups' border) has to be further apart
-//     than fp32's error, or to be of experts with the same logit and bias
-//     (whose scores are the same number). A token that fails this (about one in
-//     a thousand at 256 experts) is ranked again in fp64.
+//     than fp32's error.
+// A token that fails this (one in some thousands) is ranked again in fp64.
 #include <cfloat>
 #include <cmath>
 #include <cstdint>
@@ -169,11 +171,83 @@ __device__ __noinline__ void route_fp64(const RouteArgs& a, int64_t t, double* c
     }
 }
 
+// Logits e0 .. e0 + VPL - 1 of a row, -infinity behind its end; by 16-byte loads
+// (or one of 4 or 8) where whole lanes' runs keep rows aligned.
+template <int DT, int VPL>
+__device__ __forceinline__ void load_row(const RouteArgs& a, int64_t row, int e0, float (&z)[VPL]) {
+    constexpr int kSize = DT == NV_F32 ? 4 : 2, kBytes = VPL * kSize;
+    if constexpr (kBytes >= 4) {
+        if (a.E % VPL == 0) {
+            constexpr int kWords = kBytes / 4;
+            uint32_t w[kWords];
+            if (e0 < a.E) {
+                const char* p = static_cast<const char*>(a.z) + (row + e0) * kSize;
+                if constexpr (kBytes % 16 == 0) {
+#pragma unroll
+                    for (int i = 0; i < kWords / 4; ++i) {
+                        const uint4 u = __ldg(reinterpret_cast<const uint4*>(p) + i);
+                        w[4 * i] = u.x; w[4 * i + 1] = u.y; w[4 * i + 2] = u.z; w[4 * i + 3] = u.w;
+                    }
+                } else if constexpr (kBytes == 8) {
+                    const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+                    w[0] = u.x; w[1] = u.y;
+                } else {
+                    w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) {
+                float v;
+                if constexpr (DT == NV_F32)
+                    v = __uint_as_float(w[i]);
+                else
+                    v = __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+                z[i] = e0 < a.E ? v : -INFINITY;
+            }
+            return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) z[i] = e0 + i < a.E ? load_elem<DT>(a.z, row + e0 + i) : -INFINITY;
+}
+
+// Descending sort of N registers (Batcher's odd-even merge sort).
+__device__ __forceinline__ void order_pair(uint32_t& a, uint32_t& b) {
+    const uint32_t hi = max(a, b), lo = min(a, b);
+    a = hi;
+    b = lo;
+}
+template <int LO, int N, int R, int V>
+__device__ __forceinline__ void merge_descending(uint32_t (&k)[V]) {
+    if constexpr (2 * R < N) {
+        merge_descending<LO, N, 2 * R>(k);
+        merge_descending<LO + R, N, 2 * R>(k);
+#pragma unroll
+        for (int i = LO + R; i + R < LO + N; i += 2 * R) order_pair(k[i], k[i + R]);
+    } else {
+        order_pair(k[LO], k[LO + R]);
+    }
+}
+template <int LO, int N, int V>
+__device__ __forceinline__ void sort_descending(uint32_t (&k)[V]) {
+    if constexpr (N > 1) {
+        sort_descending<LO, N / 2>(k);
+        sort_descending<LO + N / 2, N / 2>(k);
+        merge_descending<LO, N, 1>(k);
+    }
+}
+// The float a key came from.
+__device__ __forceinline__ float key_value(uint32_t key) {
+    return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
+}
+
 // VPL: experts per lane. 32 * VPL >= E.
 template <int DT, int VPL>
-__global__ void __launch_bounds__(32 * kWarps) moe_route_kernel(RouteArgs a) {
+__global__ void __launch_bounds__(32 * kWarps) moe_route_kernel(const __grid_constant__ RouteArgs a) {
     extern __shared__ double route_smem[];  // per warp: E doubles (the fp64 ranking)
     __shared__ int s_sel[kWarps][kMaxTopk];
+    constexpr uint32_t kPlace = VPL - 1;     // a key's low bits: kPlace - (place in the lane)
+    constexpr float kKeyUnits = VPL - 1.f;   // what they may cost of its value, in units
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     // a programmatic dependent: the logits' producer ends before any access
     pdl_launch_dependents();
@@ -182,11 +256,7 @@ __global__ void __launch_bounds__(32 * kWarps) moe_route_kernel(RouteArgs a) {
     if (t >= a.T) return;
     const int e0 = lane * VPL;
     float z[VPL];
-    {
-        const int64_t row = t * a.E;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) z[i] = e0 + i < a.E ? load_elem<DT>(a.z, row + e0 + i) : -INFINITY;
-    }
+    load_row<DT, VPL>(a, t * a.E, e0, z);
     uint32_t live = 0, real = 0;  // bit i: expert e0 + i can be chosen / exists and is not masked
     float m = -FLT_MAX;
 #pragma unroll
@@ -208,7 +278,7 @@ __global__ void __launch_bounds__(32 * kWarps) moe_route_kernel(RouteArgs a) {
     float inv_sum = 1.f;
     auto score = [&](int i) {  // unnormalised for softmax
         if (!(real >> i & 1u)) return 0.f;
-        return a.softmax ? expf(z[i] - m) : 1.f / (1.f + expf(-z[i]));
+        return a.softmax ? __expf(z[i] - m) : __fdividef(1.f, 1.f + __expf(-z[i]));
     };
     float c[VPL];  // choice scores in fp32 (bias or paired groups), else the logits
     float smax = 1.f, cmax = 0.f;
@@ -240,13 +310,18 @@ __global__ void __launch_bounds__(32 * kWarps) moe_route_kernel(RouteArgs a) {
                     if (c[i] != c[i]) real &= ~(1u << i);  // a NaN bias ranks with the masked
         }
     }
-    // Error of a difference of two fp32 scores: softmax's sum over E terms and
-    // z - m each cost a few 2^-24 of the score, the bias' addition 2^-24 of the sum.
+    // What two fp32 scores may be apart by rounding alone. __expf(x) is off by (2 + |x|)
+    // units of 2^-23 of itself.
+    //   sigmoid: s (1 - s) times that stays below 1.1e-7, the quotient costs 2 units
+    //   and the sum in it half of one: 3.5e-7 a score.
+    //   softmax: e^x (2 + |x|) stays below 2 units of the largest, the sum over VPL
+    //   experts of a lane and 32 lanes VPL + 5 halves of one, its quotient 2: all of the largest score.
+    //   The bias' addition: half a unit of the sum.
     float slack = 0.f;
     if (ranked) {
 #pragma unroll
         for (int o = 16; o; o >>= 1) cmax = fmaxf(cmax, __shfl_xor_sync(0xffffffffu, cmax, o));
-        slack = smax * 1.6e-5f + cmax * 4.8e-7f;
+        slack = kKeyUnits * 1.2e-7f * (smax + cmax) + (a.softmax ? smax * (2.f * (VPL + 16) * 1.2e-7f) : 1e-6f) + (smax + cmax) * 4.8e-7f;
     }
     bool sure = true;  // every deciding comparison is beyond fp32's error
 
@@ -276,63 +351,54 @@ __global__ void __launch_bounds__(32 * kWarps) moe_route_kernel(RouteArgs a) {
             uint32_t last = 0xFFFFFFFFu;
             for (int k = 0; k < a.topk_groups; ++k) {
                 last = __reduce_max_sync(0xffffffffu, taken ? 0u : gkey);
-                const uint32_t best =
-                    __reduce_min_sync(0xffffffffu, !taken && gkey == last ? static_cast<uint32_t>(g) : kNone);
-                if (static_cast<uint32_t>(g) == best) open = taken = true;
+                const int first = __ffs(__ballot_sync(0xffffffffu, !taken && gkey == last)) - 1;  // the lowest group
+                if (g == __shfl_sync(0xffffffffu, g, first)) open = taken = true;
             }
             if (ranked && a.topk_groups < a.groups) {
                 // the border between the last open and the best closed group
                 const uint32_t next = __reduce_max_sync(0xffffffffu, taken ? 0u : gkey);
-                auto value = [](uint32_t key) {
-                    return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
-                };
-                const float hi = value(last), lo = value(next);
+                const float hi = key_value(last), lo = key_value(next);
                 if (lo > -INFINITY && !(hi - lo > 2.f * slack)) sure = false;
             }
             if (!open) live = 0;
         }
     }
 
-    // topk passes: the largest key of the warp, then the lowest expert that has it.
+    // topk passes over the lanes' sorted keys: masked experts have upper bits 1, closed and missing ones are 0
     const bool by_score = a.bias != nullptr;
-    float prev_c = INFINITY, prev_z = 0.f, prev_b = 0.f;
-    float my_s[2] = {0.f, 0.f};    // this lane's slots k = lane, lane + 32
-    int my_id[2] = {0, 0};
+    int my_id[2] = {0, 0};         // this lane's slots k = lane, lane + 32
+    float my_s[2] = {0.f, 0.f};
     if (sure) {
-        const int passes = by_score ? a.topk + 1 : a.topk;  // one more to see the best refused
-        for (int k = 0; k < passes; ++k) {
-            uint32_t key = 0;
-            int at = -1;
+        uint32_t key[VPL];
 #pragma unroll
-            for (int i = 0; i < VPL; ++i) {
-                const uint32_t ki = real >> i & 1u ? order_key(by_score ? c[i] : z[i]) : 0u;
-                if ((live >> i & 1u) && (at < 0 || ki > key)) { key = ki; at = i; }
-            }
-            const uint32_t top = __reduce_max_sync(0xffffffffu, key);
-            const uint32_t e = __reduce_min_sync(
-                0xffffffffu, at >= 0 && key == top ? static_cast<uint32_t>(e0 + at) : kNone);
-            if (e == kNone) break;  // fewer candidates than passes (the extra pass)
-            const int owner = e / VPL, slot = e % VPL;
-            if (by_score) {
-                float cz = 0.f, cc = 0.f;
-#pragma unroll
-                for (int i = 0; i < VPL; ++i)
-                    if (i == slot) { cz = z[i]; cc = c[i]; }
-                cz = __shfl_sync(0xffffffffu, cz, owner);
-                cc = __shfl_sync(0xffffffffu, cc, owner);
-                if (top == 0u) cc = -INFINITY;
-                const float cb = __ldg(a.bias + e);
-                if (k > 0 && top != 0u && !(prev_c - cc > slack) && !(prev_z == cz && prev_b == cb)) {
-                    sure = false;
-                    break;
+        for (int i = 0; i < VPL; ++i) {
+            const uint32_t upper = real >> i & 1u ? order_key(by_score ? c[i] : z[i]) & ~kPlace : VPL;
+            key[i] = live >> i & 1u ? upper | (kPlace - i) : 0u;
+        }
+        sort_descending<0, VPL>(key);
+        uint32_t prev = 0u;
+        for (int k = 0;; ++k) {
+            // without the places: among equals the lowest lane is next, then its lowest place
+            const uint32_t top = __reduce_max_sync(0xffffffffu, key[0] | kPlace);
+            if (k > 0) {  // is prev certainly before top?
+                if (top <= (VPL | kPlace)) {
+                    // masked or nothing left: certainly behind
+                } else if (by_score) {
+                    sure &= key_value(prev) - key_value(top) > slack;
+                } else if (DT != NV_BF16) {
+                    sure &= prev != top;
                 }
-                prev_c = cc;
-                prev_z = cz;
-                prev_b = cb;
             }
             if (k == a.topk) break;
-            if (lane == owner) live &= ~(1u << slot);
-            if ((k & 31) == lane) my_id[k >> 5] = static_cast<int>(e);
+            prev = top;
+            const int owner = __ffs(__ballot_sync(0xffffffffu, (key[0] | kPlace) == top)) - 1;
+            const uint32_t place = kPlace - (__shfl_sync(0xffffffffu, key[0], owner) & kPlace);
+            if (lane == owner) {
+#pragma unroll
+                for (int i = 0; i + 1 < VPL; ++i) key[i] = key[i + 1];
+                key[VPL - 1] = 0u;
+            }
+            if ((k & 31) == lane) my_id[k >> 5] = owner * VPL + static_cast<int>(place);
         }
     }
     if (!sure) {
@@ -395,7 +461,9 @@ cudaError_t launch(const RouteArgs& a, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>((a.T + kWarps - 1) / kWarps), 1, 1);
     cfg.blockDim = dim3(32 * kWarps, 1, 1);
-    cfg.dynamicSmemBytes = a.bias || a.groups > 1 ? sizeof(double) * kWarps * static_cast<size_t>(a.E) : 0;
+    // every launch whose tokens may need the fp64 ranking has room for it
+    const bool always_sure = DT == NV_BF16 && !a.bias && a.groups == 1;
+    cfg.dynamicSmemBytes = always_sure ? 0 : sizeof(double) * kWarps * static_cast<size_t>(a.E);
     cfg.stream = stream;
     cfg.attrs = pdl;
     cfg.numAttrs = 1;
