@@ -21,7 +21,7 @@
 //   * With a bias, or where a group's score is a sum of two, comparisons run in
 //     fp32, and every one that decides (neighbours in the chosen order, the last
 //     chosen and the best refused, the groups' border) has to be further apart
-//     than fp32's error.
+//     than fp32's error, or of experts with the same logit and bias.
 // A token that fails this (one in some thousands) is ranked again in fp64.
 #include <cfloat>
 #include <cmath>
@@ -37,7 +37,6 @@ namespace {
 constexpr int kWarps = 4;            // tokens per CTA
 constexpr int kMaxTopk = 64;         // as nv_moe_swiglu
 constexpr float kMaskedAt = -3.3895313892515355e38f;  // the lowest bf16: a logit at or below it is masked
-constexpr uint32_t kNone = 0x7FFFFFFFu;
 
 struct RouteArgs {
     const void* z;
@@ -60,115 +59,20 @@ __device__ __forceinline__ float warp_sum(float v) {
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 __device__ __forceinline__ double warp_sum(double v) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
-}
-// The larger value; among equals the lower index.
-__device__ __forceinline__ void warp_best(double& v, int& e) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        const double v2 = __shfl_xor_sync(0xffffffffu, v, o);
-        const int e2 = __shfl_xor_sync(0xffffffffu, e, o);
-        if (v2 > v || (v2 == v && e2 < e)) { v = v2; e = e2; }
-    }
-}
-
-__device__ __forceinline__ bool masked(float z) { return !(z > kMaskedAt); }  // also NaN
-
-// One token ranked in fp64 by one warp; c (shared memory, E doubles) holds what
-// experts are ranked by, taken and closed ones are NaN. Writes the chosen ids
-// to sel. Slow and plain: few tokens come here.
-template <int DT>
-__device__ __noinline__ void route_fp64(const RouteArgs& a, int64_t t, double* c, int* sel) {
-    const int lane = threadIdx.x & 31;
-    const int64_t row = t * a.E;
-    const bool pair_groups = a.groups > 1 && a.group_top == 2;
-    auto logit = [&](int e) { return load_elem<DT>(a.z, row + e); };
-    // without a bias the logits themselves give the order (see above)
-    auto rank_by_logit = [&]() {
-        for (int e = lane; e < a.E; e += 32) {
-            const float z = logit(e);
-            if (c[e] == c[e]) c[e] = masked(z) ? -INFINITY : static_cast<double>(fminf(z, FLT_MAX));
-        }
-    };
-    for (int e = lane; e < a.E; e += 32) c[e] = 0.0;
-    __syncwarp();
-    if (!a.bias && !pair_groups) {
-        rank_by_logit();
-    } else {
-        float m = -FLT_MAX;
-        for (int e = lane; e < a.E; e += 32) {
-            const float z = logit(e);
-            if (!masked(z)) m = fmaxf(m, fminf(z, FLT_MAX));
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        double sum = 0.0;
-        for (int e = lane; e < a.E; e += 32) {
-            const float z = logit(e);
-            double s = 0.0;
-            if (!masked(z)) {
-                const double zd = fminf(z, FLT_MAX);
-                s = a.softmax ? exp(zd - static_cast<double>(m)) : 1.0 / (1.0 + exp(-zd));
-            }
-            c[e] = s;
-            sum += s;
-        }
-        if (a.softmax) sum = warp_sum(sum);
-        for (int e = lane; e < a.E; e += 32) {
-            double s = c[e];
-            if (a.softmax && sum > 0.0) s /= sum;
-            if (a.bias) s += static_cast<double>(__ldg(a.bias + e));
-            c[e] = masked(logit(e)) || s != s ? -INFINITY : s;
-        }
-    }
-    __syncwarp();
-    if (a.groups > 1) {
-        const int per = a.E / a.groups;
-        uint32_t open = 0;  // bit i: group lane + 32 i is open
-        auto group_score = [&](int g) {
-            double b1 = -INFINITY, b2 = -INFINITY;
-            for (int i = 0; i < per; ++i) {
-                const double v = c[g * per + i];
-                if (v > b1) { b2 = b1; b1 = v; } else if (v > b2) { b2 = v; }
-            }
-            return a.group_top == 2 && b2 > -INFINITY ? b1 + b2 : b1;
-        };
-        for (int k = 0; k < a.topk_groups; ++k) {
-            double v = -INFINITY;
-            int g = static_cast<int>(kNone);
-            for (int i = 0, j = lane; j < a.groups; ++i, j += 32) {
-                if (open >> i & 1u) continue;
-                const double s = group_score(j);
-                if (g == static_cast<int>(kNone) || s > v) { v = s; g = j; }
-            }
-            warp_best(v, g);
-            if (g != static_cast<int>(kNone) && (g & 31) == lane) open |= 1u << (g >> 5);
-        }
-        __syncwarp();
-        for (int i = 0, j = lane; j < a.groups; ++i, j += 32)
-            if (!(open >> i & 1u))
-                for (int e = 0; e < per; ++e) c[j * per + e] = NAN;
-        __syncwarp();
-        if (!a.bias && pair_groups) {
-            rank_by_logit();
-            __syncwarp();
-        }
-    }
-    for (int k = 0; k < a.topk; ++k) {
-        double v = -INFINITY;
-        int e = static_cast<int>(kNone);
-        for (int j = lane; j < a.E; j += 32) {
-            const double s = c[j];
-            if (s != s) continue;
-            if (e == static_cast<int>(kNone) || s > v) { v = s; e = j; }
-        }
-        warp_best(v, e);
-        if (lane == 0) { sel[k] = e; c[e] = NAN; }
-        __syncwarp();
-    }
 }
 
 // Logits e0 .. e0 + VPL - 1 of a row, -infinity behind its end; by 16-byte loads
@@ -211,6 +115,164 @@ __device__ __forceinline__ void load_row(const RouteArgs& a, int64_t row, int e0
     for (int i = 0; i < VPL; ++i) z[i] = e0 + i < a.E ? load_elem<DT>(a.z, row + e0 + i) : -INFINITY;
 }
 
+// The bias of experts e0 .. e0 + VPL - 1, 0 behind the last.
+template <int VPL>
+__device__ __forceinline__ void load_bias(const RouteArgs& a, int e0, float (&b)[VPL]) {
+    if constexpr (VPL % 4 == 0) {
+        if (a.E % VPL == 0 && (reinterpret_cast<uintptr_t>(a.bias) & 15u) == 0) {
+#pragma unroll
+            for (int i = 0; i < VPL; i += 4) {
+                const float4 u = e0 < a.E ? __ldg(reinterpret_cast<const float4*>(a.bias + e0 + i)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                b[i] = u.x; b[i + 1] = u.y; b[i + 2] = u.z; b[i + 3] = u.w;
+            }
+            return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) b[i] = e0 + i < a.E ? __ldg(a.bias + e0 + i) : 0.f;
+}
+
+// A double's order as two words, never 0 as a pair.
+__device__ __forceinline__ void order_key(double d, uint32_t& hi, uint32_t& lo) {
+    const unsigned long long u = static_cast<unsigned long long>(__double_as_longlong(d + 0.0));
+    const unsigned long long k = u >> 63 ? ~u : u | 0x8000000000000000ull;
+    hi = static_cast<uint32_t>(k >> 32);
+    lo = static_cast<uint32_t>(k);
+}
+// The lowest lane among those with the warp's largest (hi, lo).
+__device__ __forceinline__ int best_lane(uint32_t hi, uint32_t lo) {
+    const uint32_t h = __reduce_max_sync(0xffffffffu, hi);
+    const uint32_t l = __reduce_max_sync(0xffffffffu, hi == h ? lo : 0u);
+    return __ffs(__ballot_sync(0xffffffffu, hi == h && lo == l)) - 1;
+}
+
+// One token ranked in fp64, experts laid out as in the kernel; the chosen go to sel.
+// gs (shared memory, E + groups doubles) is for groups that are not whole lanes.
+template <int DT, int VPL>
+__device__ __noinline__ void route_exact(const RouteArgs& a, int64_t t, double* gs, int* sel) {
+    const int lane = threadIdx.x & 31, e0 = lane * VPL;
+    const bool pair_groups = a.groups > 1 && a.group_top == 2;
+    float z[VPL];
+    load_row<DT, VPL>(a, t * a.E, e0, z);
+    float m = -FLT_MAX;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        z[i] = fminf(z[i] > kMaskedAt ? z[i] : -INFINITY, FLT_MAX);
+        m = fmaxf(m, z[i]);
+    }
+    double c[VPL];  // without a bias the logits themselves give the order (see above)
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) c[i] = z[i];
+    if (a.bias || pair_groups) {
+        double part = 0.0;
+        if (a.softmax) m = warp_max(m);
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            const double zd = z[i];
+            c[i] = a.softmax ? exp(zd - static_cast<double>(m)) : 1.0 / (1.0 + exp(-zd));
+            part += c[i];
+        }
+        const double sum = a.softmax ? warp_sum(part) : 1.0;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            if (sum > 0.0) c[i] /= sum;
+            if (a.bias && e0 + i < a.E) c[i] += static_cast<double>(__ldg(a.bias + e0 + i));
+            if (!(z[i] > -INFINITY) || c[i] != c[i]) c[i] = -INFINITY;
+        }
+    }
+    uint32_t open = 0;  // bit i: expert e0 + i can be chosen
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+        if (e0 + i < a.E) open |= 1u << i;
+    if (a.groups > 1) {
+        const int per = a.E / a.groups, lanes = per / VPL;
+        if (per % VPL == 0 && (lanes & (lanes - 1)) == 0) {
+            double b1 = -INFINITY, b2 = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) {
+                b2 = fmax(b2, fmin(b1, c[i]));
+                b1 = fmax(b1, c[i]);
+            }
+            for (int o = 1; o < lanes; o <<= 1) {
+                const double o1 = __shfl_xor_sync(0xffffffffu, b1, o), o2 = __shfl_xor_sync(0xffffffffu, b2, o);
+                b2 = fmax(fmax(b2, o2), fmin(b1, o1));
+                b1 = fmax(b1, o1);
+            }
+            uint32_t hi = 0, lo = 0;
+            if (open) order_key(pair_groups && b2 > -INFINITY ? b1 + b2 : b1, hi, lo);
+            const int first = lane & ~(lanes - 1);
+            bool chosen = false;
+            for (int k = 0; k < a.topk_groups; ++k) {
+                if (best_lane(hi, lo) == first) {
+                    chosen = true;
+                    hi = lo = 0;
+                }
+            }
+            if (!chosen) open = 0;
+        } else {
+            double* cs = gs + a.groups;
+#pragma unroll
+            for (int i = 0; i < VPL; ++i)
+                if (e0 + i < a.E) cs[e0 + i] = c[i];
+            __syncwarp();
+            for (int g = 0; g < a.groups; ++g) {
+                double b1 = -INFINITY, b2 = -INFINITY;
+                for (int i = lane; i < per; i += 32) {
+                    const double v = cs[g * per + i];
+                    b2 = fmax(b2, fmin(b1, v));
+                    b1 = fmax(b1, v);
+                }
+                for (int o = 16; o; o >>= 1) {
+                    if (o >= per) continue;  // those lanes hold nothing
+                    const double o1 = __shfl_xor_sync(0xffffffffu, b1, o), o2 = __shfl_xor_sync(0xffffffffu, b2, o);
+                    b2 = fmax(fmax(b2, o2), fmin(b1, o1));
+                    b1 = fmax(b1, o1);
+                }
+                if (lane == 0) gs[g] = pair_groups && b2 > -INFINITY ? b1 + b2 : b1;
+            }
+            __syncwarp();
+            for (int k = 0; k < a.topk_groups; ++k) {  // the chosen become NaN
+                uint32_t hi = 0, lo = 0;
+                int g = 0;
+                for (int j = lane; j < a.groups; j += 32) {
+                    uint32_t h = 0, l = 0;
+                    if (gs[j] == gs[j]) order_key(gs[j], h, l);
+                    if (h > hi || (h == hi && l > lo)) { hi = h; lo = l; g = j; }
+                }
+                // among equals the lowest group, which need not be the lowest lane's
+                const uint32_t h = __reduce_max_sync(0xffffffffu, hi);
+                const uint32_t l = __reduce_max_sync(0xffffffffu, hi == h ? lo : 0u);
+                g = static_cast<int>(__reduce_min_sync(0xffffffffu, hi == h && lo == l ? static_cast<uint32_t>(g) : 0x7FFFFFFFu));
+                if (lane == 0) gs[g] = NAN;
+                __syncwarp();
+            }
+#pragma unroll
+            for (int i = 0; i < VPL; ++i)
+                if (e0 + i < a.E && gs[(e0 + i) / per] == gs[(e0 + i) / per]) open &= ~(1u << i);
+        }
+    }
+    if (!a.bias && pair_groups) {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) c[i] = z[i];
+    }
+    for (int k = 0; k < a.topk; ++k) {
+        uint32_t hi = 0, lo = 0;
+        int at = 0;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            uint32_t h = 0, l = 0;
+            if (open >> i & 1u) order_key(c[i], h, l);
+            if (h > hi || (h == hi && l > lo)) { hi = h; lo = l; at = i; }
+        }
+        const int owner = best_lane(hi, lo);
+        if (lane == owner) {
+            sel[k] = e0 + at;
+            open &= ~(1u << at);
+        }
+    }
+    __syncwarp();
+}
+
 // Descending sort of N registers (Batcher's odd-even merge sort).
 __device__ __forceinline__ void order_pair(uint32_t& a, uint32_t& b) {
     const uint32_t hi = max(a, b), lo = min(a, b);
@@ -244,10 +306,9 @@ __device__ __forceinline__ float key_value(uint32_t key) {
 // VPL: experts per lane. 32 * VPL >= E.
 template <int DT, int VPL>
 __global__ void __launch_bounds__(32 * kWarps) moe_route_kernel(const __grid_constant__ RouteArgs a) {
-    extern __shared__ double route_smem[];  // per warp: E doubles (the fp64 ranking)
+    extern __shared__ double route_smem[];  // per warp: E + groups doubles (the fp64 ranking)
     __shared__ int s_sel[kWarps][kMaxTopk];
     constexpr uint32_t kPlace = VPL - 1;     // a key's low bits: kPlace - (place in the lane)
-    constexpr float kKeyUnits = VPL - 1.f;   // what they may cost of its value, in units
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     // a programmatic dependent: the logits' producer ends before any access
     pdl_launch_dependents();
@@ -257,74 +318,67 @@ __global__ void __launch_bounds__(32 * kWarps) moe_route_kernel(const __grid_con
     const int e0 = lane * VPL;
     float z[VPL];
     load_row<DT, VPL>(a, t * a.E, e0, z);
-    uint32_t live = 0, real = 0;  // bit i: expert e0 + i can be chosen / exists and is not masked
+    // a masked expert's logit becomes -infinity: its score is 0, its rank last
     float m = -FLT_MAX;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-        if (e0 + i < a.E) live |= 1u << i;
-        if (!masked(z[i])) {
-            real |= 1u << i;
-            z[i] = fminf(z[i], FLT_MAX);
-            m = fmaxf(m, z[i]);
-        }
+        z[i] = fminf(z[i] > kMaskedAt ? z[i] : -INFINITY, FLT_MAX);
+        m = fmaxf(m, z[i]);
     }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (a.softmax) m = warp_max(m);
 
     // Scores that a choice or the weights need. Renormalised softmax weights are
     // ratios of exponentials: the sum over all experts cancels.
-    const bool sum_needed = a.softmax && (!a.renormalize || a.bias);
+    const bool by_score = a.bias != nullptr;
     const bool pair_groups = a.groups > 1 && a.group_top == 2;
+    const bool ranked = by_score || pair_groups;
     float inv_sum = 1.f;
-    auto score = [&](int i) {  // unnormalised for softmax
-        if (!(real >> i & 1u)) return 0.f;
-        return a.softmax ? __expf(z[i] - m) : __fdividef(1.f, 1.f + __expf(-z[i]));
-    };
-    float c[VPL];  // choice scores in fp32 (bias or paired groups), else the logits
-    float smax = 1.f, cmax = 0.f;
-    const bool ranked = a.bias || pair_groups;
-    if (sum_needed || ranked) {
-        float part = 0.f;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-            c[i] = score(i);
-            part += c[i];
-        }
-        if (sum_needed) {
-            const float sum = warp_sum(part);
-            inv_sum = sum > 0.f ? 1.f / sum : 0.f;
-        }
-        if (a.softmax && a.bias) smax = inv_sum;  // the largest score (1 where c is not normalised)
-        if (a.bias) {
-            bool odd = false;
+    float c[VPL];     // choice scores in fp32 (-infinity: masked)
+    float slack = 0.f;
+    if (a.softmax) {
+        if (ranked || !a.renormalize) {
+            float part = 0.f;
 #pragma unroll
             for (int i = 0; i < VPL; ++i) {
-                const float b = e0 + i < a.E ? __ldg(a.bias + e0 + i) : 0.f;
-                c[i] = fmaf(c[i], inv_sum, b);
-                cmax = fmaxf(cmax, fabsf(b));
-                odd |= c[i] != c[i];
+                c[i] = __expf(z[i] - m);
+                part += c[i];
             }
-            if (odd)
-#pragma unroll
-                for (int i = 0; i < VPL; ++i)
-                    if (c[i] != c[i]) real &= ~(1u << i);  // a NaN bias ranks with the masked
+            if (by_score || !a.renormalize) {
+                const float sum = warp_sum(part);
+                inv_sum = sum > 0.f ? 1.f / sum : 0.f;
+            }
         }
-    }
-    // What two fp32 scores may be apart by rounding alone. __expf(x) is off by (2 + |x|)
-    // units of 2^-23 of itself.
-    //   sigmoid: s (1 - s) times that stays below 1.1e-7, the quotient costs 2 units
-    //   and the sum in it half of one: 3.5e-7 a score.
-    //   softmax: e^x (2 + |x|) stays below 2 units of the largest, the sum over VPL
-    //   experts of a lane and 32 lanes VPL + 5 halves of one, its quotient 2: all of the largest score.
-    //   The bias' addition: half a unit of the sum.
-    float slack = 0.f;
-    if (ranked) {
+    } else if (ranked) {
 #pragma unroll
-        for (int o = 16; o; o >>= 1) cmax = fmaxf(cmax, __shfl_xor_sync(0xffffffffu, cmax, o));
-        slack = kKeyUnits * 1.2e-7f * (smax + cmax) + (a.softmax ? smax * (2.f * (VPL + 16) * 1.2e-7f) : 1e-6f) + (smax + cmax) * 4.8e-7f;
+        for (int i = 0; i < VPL; ++i) c[i] = rcp_approx(1.f + __expf(-z[i]));
+    }
+    if (ranked) {
+        float smax = a.softmax && by_score ? inv_sum : 1.f;  // the largest score
+        float cmax = 0.f;
+        if (by_score) {
+            float b[VPL];
+            load_bias<VPL>(a, e0, b);
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) {
+                c[i] = fmaf(c[i], inv_sum, b[i]);
+                cmax = fmaxf(cmax, fabsf(b[i]));
+            }
+            cmax = warp_max(cmax);
+        }
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) c[i] = z[i] > -INFINITY && c[i] == c[i] ? c[i] : -INFINITY;  // a NaN bias too
+        // What two fp32 scores may be apart by rounding alone. __expf(x) is off by (2 + |x|)
+        // units of 2^-23 of itself.
+        //   sigmoid: s (1 - s) times that stays below 1.1e-7, the reciprocal costs a unit
+        //   and the sum in it half of one: 3.5e-7 a score.
+        //   softmax: e^x (2 + |x|) stays below 2 units of the largest, the sum over VPL
+        //   experts of a lane and 32 lanes VPL + 5 halves of one, its quotient 2: all of the largest score.
+        //   The bias' addition: half a unit of the sum. The bits a key lacks: VPL - 1 units of it.
+        slack = (VPL + 3) * 1.2e-7f * (smax + cmax) + (a.softmax ? smax * (2.f * (VPL + 16) * 1.2e-7f) : 1e-6f);
     }
     bool sure = true;  // every deciding comparison is beyond fp32's error
 
+    bool open = e0 < a.E;  // this lane's experts can be chosen
     if (a.groups > 1) {
         const int per = a.E / a.groups;
         const int lanes = per / VPL;  // lanes per group, where a group is whole lanes
@@ -334,7 +388,7 @@ __global__ void __launch_bounds__(32 * kWarps) moe_route_kernel(const __grid_con
             float b1 = -INFINITY, b2 = -INFINITY;
 #pragma unroll
             for (int i = 0; i < VPL; ++i) {
-                const float v = real >> i & 1u ? (ranked ? c[i] : z[i]) : -INFINITY;
+                const float v = ranked ? c[i] : z[i];
                 b2 = fmaxf(b2, fminf(b1, v));
                 b1 = fmaxf(b1, v);
             }
@@ -345,111 +399,108 @@ __global__ void __launch_bounds__(32 * kWarps) moe_route_kernel(const __grid_con
                 b1 = fmaxf(b1, o1);
             }
             const float gs = pair_groups && b2 > -INFINITY ? b1 + b2 : b1;
-            const uint32_t gkey = e0 < a.E ? order_key(gs) : 0u;
-            const int g = e0 / per;
-            bool open = false, taken = e0 >= a.E;
-            uint32_t last = 0xFFFFFFFFu;
+            uint32_t gkey = open ? order_key(gs) : 0u;  // 0: taken or not there
+            const int first = lane & ~(lanes - 1);       // the group's first lane
+            open = false;
+            uint32_t last = 0u;
             for (int k = 0; k < a.topk_groups; ++k) {
-                last = __reduce_max_sync(0xffffffffu, taken ? 0u : gkey);
-                const int first = __ffs(__ballot_sync(0xffffffffu, !taken && gkey == last)) - 1;  // the lowest group
-                if (g == __shfl_sync(0xffffffffu, g, first)) open = taken = true;
+                last = __reduce_max_sync(0xffffffffu, gkey);
+                if (first == __ffs(__ballot_sync(0xffffffffu, gkey == last)) - 1) {  // the lowest such group
+                    open = true;
+                    gkey = 0u;
+                }
             }
             if (ranked && a.topk_groups < a.groups) {
                 // the border between the last open and the best closed group
-                const uint32_t next = __reduce_max_sync(0xffffffffu, taken ? 0u : gkey);
+                const uint32_t next = __reduce_max_sync(0xffffffffu, gkey);
                 const float hi = key_value(last), lo = key_value(next);
                 if (lo > -INFINITY && !(hi - lo > 2.f * slack)) sure = false;
             }
-            if (!open) live = 0;
         }
     }
 
-    // topk passes over the lanes' sorted keys: masked experts have upper bits 1, closed and missing ones are 0
-    const bool by_score = a.bias != nullptr;
-    int my_id[2] = {0, 0};         // this lane's slots k = lane, lane + 32
-    float my_s[2] = {0.f, 0.f};
+    // topk passes over the lanes' sorted keys; closed and missing experts are 0
+    int id0 = 0, id1 = 0;          // the chosen of this lane's slots k = lane and lane + 32
     if (sure) {
+        constexpr uint32_t kLast = 0x007FFFFFu | kPlace;  // -infinity's key: behind it nothing is left to tell apart
         uint32_t key[VPL];
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
-            const uint32_t upper = real >> i & 1u ? order_key(by_score ? c[i] : z[i]) & ~kPlace : VPL;
-            key[i] = live >> i & 1u ? upper | (kPlace - i) : 0u;
+            const uint32_t k = order_key(by_score ? c[i] : z[i]);
+            key[i] = open ? (k & ~kPlace) | (kPlace - i) : 0u;
         }
         sort_descending<0, VPL>(key);
         uint32_t prev = 0u;
+        float prev_value = INFINITY;
+        int prev_e = 0;
         for (int k = 0;; ++k) {
             // without the places: among equals the lowest lane is next, then its lowest place
             const uint32_t top = __reduce_max_sync(0xffffffffu, key[0] | kPlace);
-            if (k > 0) {  // is prev certainly before top?
-                if (top <= (VPL | kPlace)) {
-                    // masked or nothing left: certainly behind
-                } else if (by_score) {
-                    sure &= key_value(prev) - key_value(top) > slack;
+            const int owner = __ffs(__ballot_sync(0xffffffffu, (key[0] | kPlace) == top)) - 1;
+            const int e = owner * VPL + static_cast<int>(kPlace - (__shfl_sync(0xffffffffu, key[0], owner) & kPlace));
+            if (top > kLast) {  // is the expert before certainly before this one?
+                if (by_score) {
+                    const float value = key_value(top);
+                    if (!(prev_value - value > slack))  // the same logit and bias: the same score, in order of the ids
+                        sure &= k > 0 && load_elem<DT>(a.z, t * a.E + e) == load_elem<DT>(a.z, t * a.E + prev_e) &&
+                                __ldg(a.bias + e) == __ldg(a.bias + prev_e);
+                    prev_value = value;
+                    prev_e = e;
                 } else if (DT != NV_BF16) {
                     sure &= prev != top;
+                    prev = top;
                 }
             }
             if (k == a.topk) break;
-            prev = top;
-            const int owner = __ffs(__ballot_sync(0xffffffffu, (key[0] | kPlace) == top)) - 1;
-            const uint32_t place = kPlace - (__shfl_sync(0xffffffffu, key[0], owner) & kPlace);
             if (lane == owner) {
 #pragma unroll
                 for (int i = 0; i + 1 < VPL; ++i) key[i] = key[i + 1];
                 key[VPL - 1] = 0u;
             }
-            if ((k & 31) == lane) my_id[k >> 5] = owner * VPL + static_cast<int>(place);
+            if (k == lane) id0 = e;
+            if (k == lane + 32) id1 = e;
         }
     }
     if (!sure) {
         int* sel = s_sel[warp];
-        route_fp64<DT>(a, t, route_smem + static_cast<int64_t>(warp) * a.E, sel);
+        route_exact<DT, VPL>(a, t, route_smem + warp * (a.E + a.groups), sel);
         __syncwarp();
-        if (lane < a.topk) my_id[0] = sel[lane];
-        if (lane + 32 < a.topk) my_id[1] = sel[lane + 32];
+        if (lane < a.topk) id0 = sel[lane];
+        if (lane + 32 < a.topk) id1 = sel[lane + 32];
     }
 
     // Weights of the chosen, from their logits. Renormalised weights are ratios,
     // so a common factor that keeps them in range is free: softmax divides by
     // the largest chosen exponential, sigmoid by e^top where all logits are negative.
-    float zs[2];
-    float top = -FLT_MAX;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        zs[h] = 32 * h + lane < a.topk ? load_elem<DT>(a.z, t * a.E + my_id[h]) : -INFINITY;
-        if (!masked(zs[h])) {
-            zs[h] = fminf(zs[h], FLT_MAX);
-            top = fmaxf(top, zs[h]);
-        }
-    }
-    float base = m;
+    const bool has0 = lane < a.topk, has1 = lane + 32 < a.topk;
+    float z0 = has0 ? load_elem<DT>(a.z, t * a.E + id0) : -INFINITY;
+    float z1 = has1 ? load_elem<DT>(a.z, t * a.E + id1) : -INFINITY;
+    z0 = fminf(z0 > kMaskedAt ? z0 : -INFINITY, FLT_MAX);
+    z1 = fminf(z1 > kMaskedAt ? z1 : -INFINITY, FLT_MAX);
+    float base = a.softmax ? m : 0.f;
     if (a.renormalize) {
-#pragma unroll
-        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float top = warp_max(fmaxf(fmaxf(z0, z1), -FLT_MAX));
         base = a.softmax ? top : fminf(top, 0.f);
         inv_sum = 1.f;
-    } else if (!a.softmax) {
-        base = 0.f;
     }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        if (masked(zs[h])) continue;
-        if (a.softmax)
-            my_s[h] = expf(zs[h] - base) * inv_sum;
-        else  // without overflow on either side
-            my_s[h] = zs[h] >= 0.f ? 1.f / (1.f + expf(-zs[h])) : expf(zs[h] - base) / (1.f + expf(zs[h]));
-    }
+    auto weight = [&](float x) {
+        if (!(x > -INFINITY)) return 0.f;
+        if (a.softmax) return expf(x - base) * inv_sum;
+        return x >= 0.f ? 1.f / (1.f + expf(-x)) : expf(x - base) / (1.f + expf(x));  // overflows on neither side
+    };
+    const float s0 = weight(z0), s1 = a.topk > 32 ? weight(z1) : 0.f;
     float factor = a.scale;
     if (a.renormalize) {
-        const float sum = warp_sum(my_s[0] + my_s[1]);
+        const float sum = warp_sum(s0 + s1);
         factor = sum > 0.f ? a.scale / sum : 0.f;
     }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        if (32 * h + lane < a.topk) {
-            a.ids[t * a.topk + 32 * h + lane] = static_cast<uint32_t>(my_id[h]);
-            a.w[t * a.topk + 32 * h + lane] = my_s[h] * factor;
-        }
+    if (has0) {
+        a.ids[t * a.topk + lane] = static_cast<uint32_t>(id0);
+        a.w[t * a.topk + lane] = s0 * factor;
+    }
+    if (has1) {
+        a.ids[t * a.topk + 32 + lane] = static_cast<uint32_t>(id1);
+        a.w[t * a.topk + 32 + lane] = s1 * factor;
     }
 }
 
@@ -463,7 +514,7 @@ cudaError_t launch(const RouteArgs& a, cudaStream_t stream) {
     cfg.blockDim = dim3(32 * kWarps, 1, 1);
     // every launch whose tokens may need the fp64 ranking has room for it
     const bool always_sure = DT == NV_BF16 && !a.bias && a.groups == 1;
-    cfg.dynamicSmemBytes = always_sure ? 0 : sizeof(double) * kWarps * static_cast<size_t>(a.E);
+    cfg.dynamicSmemBytes = always_sure ? 0 : sizeof(double) * kWarps * static_cast<size_t>(a.E + a.groups);
     cfg.stream = stream;
     cfg.attrs = pdl;
     cfg.numAttrs = 1;
