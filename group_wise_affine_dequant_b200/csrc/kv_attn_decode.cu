@@ -10,8 +10,8 @@
 // Per CTA: a producer warp fetches page ids and scales of the next item and
 // streams its codes by TMA, 64 tokens of K and V a stage (boxes of
 // min(block, 64) tokens, swizzled so that all fragment reads but the 64-wide
-// values' are free of bank conflicts). Four consumer warps take 16 of the 64
-// tokens each, with their own running maximum, sum and output: scores by mma.m16n8k16
+// values' are free of bank conflicts). Four consumer warps take 32 tokens of every
+// other stage each, with their own running maximum, sum and output: scores by mma.m16n8k16
 // (fp16 codes are exact), weights straight from the score fragments into the second
 // product's A operand, values transposed byte-wise in registers. No barrier
 // between the warps inside an item; they join at its end. Items of a sequence that
@@ -118,7 +118,7 @@ kv_attn_decode_kernel(const __grid_constant__ DecodeArgs p, const __grid_constan
     if (tid == 0) {
         for (int i = 0; i < NS; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], kConsumers);
+            mbar_init(&empty[i], 2);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&meta_full[i], 1);
@@ -288,8 +288,8 @@ kv_attn_decode_kernel(const __grid_constant__ DecodeArgs p, const __grid_constan
     } else {
         // ----------------------------------------------------------- consumers
         const int g = lane >> 2, t4 = lane & 3;
-        int stage = 0;
-        uint32_t phase = 0;
+        const int pair = warp >> 1;  // warps 0, 1 take an item's even stages, 2, 3 the odd ones; 32 tokens a warp
+        uint32_t before = 0;         // stages of the items before
         int it = 0;
         for (int64_t w = blockIdx.x; ok && w < total; w += gridDim.x, ++it) {
             const int slot = it & 1;
@@ -353,118 +353,153 @@ kv_attn_decode_kernel(const __grid_constant__ DecodeArgs p, const __grid_constan
             for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
             float ref[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 
-            for (int t = m.t0; ok && t < m.t1; t += kTile) {
-                ok = mbar_wait(&full[stage], phase, 0x65);
+            const int stages_here = (m.t1 - m.t0 + kTile - 1) / kTile;
+            for (int n_stage = pair; n_stage < stages_here; n_stage += 2) {
+                const int stage = (before + n_stage) % NS;
+                ok = mbar_wait(&full[stage], (before + n_stage) / NS & 1, 0x65);
                 if (!ok) break;
-                const int j0 = t + 16 * warp;
-                const BlockScales bs = scales[slot][j0 < m.t1 ? j0 / p.c.block - m.block0 : 0];
-                if (j0 < m.t1 && bs.ks >= 0.f) {  // else nothing of these 16 tokens is seen
-                    const uint8_t* kt = stages + stage * 2 * kHalf + 16 * warp * D;
-                    const uint8_t* vt = kt + kHalf;
-                    float c[2][4];
+                const int j0 = m.t0 + n_stage * kTile + 32 * (warp & 1);
+                const uint8_t* kt = stages + stage * 2 * kHalf + 32 * (warp & 1) * D;
+                const uint8_t* vt = kt + kHalf;
+                // the scales of the two halves of 16 tokens; a half behind the end or of a bad page is not seen
+                BlockScales bs[2];
+                bool seen[2];
 #pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.f;
-                        const int row = 8 * n + g;
+                for (int x = 0; x < 2; ++x) {
+                    const int j = j0 + 16 * x;
+                    bs[x] = scales[slot][j < m.t1 ? j / p.c.block - m.block0 : 0];
+                    seen[x] = j < m.t1 && bs[x].ks >= 0.f;
+                }
+                float c[4][4];
+                uint4 kw[4][D / 64];
 #pragma unroll
-                        for (int i = 0; i < D / 64; ++i) {
-                            uint4 u;
-                            if constexpr (D == 128)
-                                u = *reinterpret_cast<const uint4*>(kt + row * 128 + ((2 * t4 + i) ^ (row & 7)) * 16);
-                            else
-                                u = *reinterpret_cast<const uint4*>(kt + row * 64 + (t4 ^ ((row >> 1) & 3)) * 16);
-                            const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+                for (int n = 0; n < 4; ++n) {
+                    c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.f;
+                    const int row = 8 * n + g;
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const uint32_t y = prepare_word<MODE>(x[j]);
-                                const int ks = 4 * i + j;
-                                mma_f16_16816(c[n], qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3], pair_lo_h2<MODE>(y),
-                                              pair_hi_h2<MODE>(y));
-                            }
-                        }
+                    for (int i = 0; i < D / 64; ++i) {
+                        if constexpr (D == 128)
+                            kw[n][i] = *reinterpret_cast<const uint4*>(kt + row * 128 + ((2 * t4 + i) ^ (row & 7)) * 16);
+                        else
+                            kw[n][i] = *reinterpret_cast<const uint4*>(kt + row * 64 + (t4 ^ ((row >> 1) & 3)) * 16);
                     }
-                    const bool whole = j0 >= m.lo_max && j0 + 16 <= m.hi_min;
-                    float mx[2] = {-INFINITY, -INFINITY};
+                }
 #pragma unroll
-                    for (int n = 0; n < 2; ++n)
+                for (int i = 0; i < D / 64; ++i)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int r = e >> 1, j = j0 + 8 * n + 2 * t4 + (e & 1);
-                            float z = c[n][e] * (zc[r] * bs.ks);
-                            if (!whole && (j < row_lo[r] || j >= row_hi[r])) z = -INFINITY;
-                            c[n][e] = z;
-                            mx[r] = fmaxf(mx[r], z);
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int n = 0; n < 4; ++n) {
+                            const uint32_t x = j == 0 ? kw[n][i].x : j == 1 ? kw[n][i].y : j == 2 ? kw[n][i].z : kw[n][i].w;
+                            const uint32_t y = prepare_word<MODE>(x);
+                            const int ks = 4 * i + j;
+                            mma_f16_16816(c[n], qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3], pair_lo_h2<MODE>(y), pair_hi_h2<MODE>(y));
                         }
-                    bool grow = false;
+                // values: of k-step x, tokens 2 t4, 2 t4 + 1 (b0) and 8 + 2 t4, 9 + 2 t4 (b1); n-tile i, column g is
+                // value (D / 8) g + i
+                uint32_t v[2][4][D / 32];
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
-                        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2)) + bs.lg;
-                        grow |= mx[r] > ref[r] + kSlack;
-                    }
-                    if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            // each row by itself: its result must not depend on its neighbours
-                            const bool up = mx[r] > ref[r] + kSlack;
-                            const float f = up ? exp2f(ref[r] - mx[r]) : 1.f;
-                            ref[r] = up ? mx[r] : ref[r];
-                            l[r] *= f;
-#pragma unroll
-                            for (int i = 0; i < NT; ++i) {
-                                o[i][2 * r] *= f;
-                                o[i][2 * r + 1] *= f;
-                            }
-                        }
-                    }
-                    uint32_t pa[4];
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const float base = bs.lg + kLift - (ref[r] > -INFINITY ? ref[r] : 0.f);
-                        float sum = 0.f;
-#pragma unroll
-                        for (int n = 0; n < 2; ++n) {
-                            const float w0 = exp2_approx(c[n][2 * r] + base), w1 = exp2_approx(c[n][2 * r + 1] + base);
-                            sum += w0 + w1;
-                            pa[2 * n + r] = f2_to_h2(w0, w1);
-                        }
-                        l[r] = fmaf(sum, bs.inv, l[r]);
-                    }
-                    // values: tokens 2 t4, 2 t4 + 1 (b0) and 8 + 2 t4, 9 + 2 t4 (b1); n-tile i, column g is value
-                    // (D / 8) g + i
-                    uint32_t v[4][D / 32];
+                for (int x = 0; x < 2; ++x)
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const int row = 8 * (q >> 1) + 2 * t4 + (q & 1);
+                        const int row = 16 * x + 8 * (q >> 1) + 2 * t4 + (q & 1);
                         if constexpr (D == 128) {
                             const uint4 u = *reinterpret_cast<const uint4*>(vt + row * 128 + (g ^ (row & 7)) * 16);
-                            v[q][0] = u.x; v[q][1] = u.y; v[q][2] = u.z; v[q][3] = u.w;
+                            v[x][q][0] = u.x; v[x][q][1] = u.y; v[x][q][2] = u.z; v[x][q][3] = u.w;
                         } else {
                             const uint2 u = *reinterpret_cast<const uint2*>(
                                 vt + row * 64 + ((g >> 1) ^ ((row >> 1) & 3)) * 16 + (g & 1) * 8);
-                            v[q][0] = u.x; v[q][1] = u.y;
+                            v[x][q][0] = u.x; v[x][q][1] = u.y;
                         }
-                        // a slot behind the last token may hold a NaN code
-                        if (MODE == NV_KV_E4M3 && !whole && j0 + row >= m.len)
-#pragma unroll
-                            for (int i = 0; i < D / 32; ++i) v[q][i] = 0;
                     }
+                const bool whole = seen[0] && seen[1] && j0 >= m.lo_max && j0 + 32 <= m.hi_min;
+                float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                    for (int i = 0; i < D / 32; ++i) {
-                        const uint32_t a0 = prepare_word<MODE>(v[0][i]), a1 = prepare_word<MODE>(v[1][i]);
-                        const uint32_t b0 = prepare_word<MODE>(v[2][i]), b1 = prepare_word<MODE>(v[3][i]);
+                for (int x = 0; x < 2; ++x)
 #pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            const uint32_t x = tc::prmt(a0, a1, half ? 0x7362 : 0x5140), y = tc::prmt(b0, b1, half ? 0x7362 : 0x5140);
-                            mma_f16_16816(o[4 * i + 2 * half], pa[0], pa[1], pa[2], pa[3], pair_lo_h2<MODE>(x), pair_lo_h2<MODE>(y));
-                            mma_f16_16816(o[4 * i + 2 * half + 1], pa[0], pa[1], pa[2], pa[3], pair_hi_h2<MODE>(x), pair_hi_h2<MODE>(y));
+                    for (int r = 0; r < 2; ++r) {
+                        const float f = zc[r] * bs[x].ks;
+#pragma unroll
+                        for (int n = 2 * x; n < 2 * x + 2; ++n)
+#pragma unroll
+                            for (int e = 2 * r; e < 2 * r + 2; ++e) c[n][e] = fmaf(c[n][e], f, bs[x].lg);
+                    }
+                if (!whole) {
+#pragma unroll
+                    for (int n = 0; n < 4; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int r = e >> 1, j = j0 + 8 * n + 2 * t4 + (e & 1);
+                            if (!seen[n >> 1] || j < row_lo[r] || j >= row_hi[r]) c[n][e] = -INFINITY;
+                        }
+                    if (MODE == NV_KV_E4M3) {  // a slot behind the last token, or of no page, may hold a NaN code
+#pragma unroll
+                        for (int x = 0; x < 2; ++x)
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                if (!seen[x] || j0 + 16 * x + 8 * (q >> 1) + 2 * t4 + (q & 1) >= m.len)
+#pragma unroll
+                                    for (int i = 0; i < D / 32; ++i) v[x][q][i] = 0;
+                    }
+                }
+                bool grow = false;
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) mx[r] = fmaxf(mx[r], fmaxf(c[n][2 * r], c[n][2 * r + 1]));
+                    mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+                    mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+                    grow |= mx[r] > ref[r] + kSlack;
+                }
+                if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        // each row by itself: its result must not depend on its neighbours
+                        const bool up = mx[r] > ref[r] + kSlack;
+                        const float f = up ? exp2f(ref[r] - mx[r]) : 1.f;
+                        ref[r] = up ? mx[r] : ref[r];
+                        l[r] *= f;
+#pragma unroll
+                        for (int i = 0; i < NT; ++i) {
+                            o[i][2 * r] *= f;
+                            o[i][2 * r + 1] *= f;
                         }
                     }
                 }
+                uint32_t pa[2][4];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float base = kLift - (ref[r] > -INFINITY ? ref[r] : 0.f);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        float sum = 0.f;
+#pragma unroll
+                        for (int n = 0; n < 2; ++n) {
+                            const float w0 = exp2_approx(c[2 * x + n][2 * r] + base), w1 = exp2_approx(c[2 * x + n][2 * r + 1] + base);
+                            sum += w0 + w1;
+                            pa[x][2 * n + r] = f2_to_h2(w0, w1);
+                        }
+                        l[r] = fmaf(sum, bs[x].inv, l[r]);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const uint32_t a0 = prepare_word<MODE>(v[x][0][i]), a1 = prepare_word<MODE>(v[x][1][i]);
+                        const uint32_t b0 = prepare_word<MODE>(v[x][2][i]), b1 = prepare_word<MODE>(v[x][3][i]);
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            const uint32_t y0 = tc::prmt(a0, a1, half ? 0x7362 : 0x5140), y1 = tc::prmt(b0, b1, half ? 0x7362 : 0x5140);
+                            mma_f16_16816(o[4 * i + 2 * half], pa[x][0], pa[x][1], pa[x][2], pa[x][3], pair_lo_h2<MODE>(y0), pair_lo_h2<MODE>(y1));
+                            mma_f16_16816(o[4 * i + 2 * half + 1], pa[x][0], pa[x][1], pa[x][2], pa[x][3], pair_hi_h2<MODE>(y0), pair_hi_h2<MODE>(y1));
+                        }
+                    }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&empty[stage]);
-                if (++stage == NS) { stage = 0; phase ^= 1; }
             }
+            before += stages_here;
+            if (!ok) break;
             // join the four warps: references and sums first, then the outputs in warp order
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
