@@ -86,7 +86,7 @@ KvAttnPlan kv_attn_plan(nv_dtype dt, int64_t rows, int Hq, int H, int block, int
     r.prefill = !only_few;
     r.decode = only_few || S > 1;
     if (r.decode) {
-        r.d = nvq::kv_decode_plan({rows, S, max_pages, Hq, H, block, D, only_few}, sms);
+        r.d = nvq::kv_decode_plan({rows, S, max_pages, Hq, H, block, D, only_few, Hq / H, most * (Hq / H)}, sms);
         r.decode_bytes = (r.d.bytes(D) + 255) / 256 * 256;
     }
     if (r.prefill) {

@@ -148,9 +148,10 @@ struct KvDecodeSizes {
     int64_t rows, S, max_pages;
     int Hq, H, block, D;
     bool only;
+    int64_t G, most_rows;  // heads of a group; most flattened rows a sequence has
 };
 struct KvDecodePlan {
-    int target, max_chunks, row_limit;
+    int target, max_chunks, tile_rows, row_limit;
     int64_t part_rows;
     size_t bytes(int D) const {
         return max_chunks > 1 ? static_cast<size_t>(part_rows) * max_chunks * (D + 1) * sizeof(float) : 0;
