@@ -8,14 +8,19 @@
 // other's products do.
 //   warps 0-3, 4-7   softmax of subtile 0, 1: thread = row = TMEM lane; scores
 //                    arrive in TMEM, weights go back over them as fp16
-//   warps 8-11       converters: 8-bit codes from global memory (the next tile's
+//   warps 8-15       converters: 8-bit codes from global memory (the next tile's
 //                    loads are in flight while this one's are converted), exact
 //                    fp16 into swizzled shared tiles [token][value], a ring of two
 //                    K and two V tiles
-//   warp 12          issues the products: S = Q K^T (K-major operands), O += P V
+//   warp 16          issues the products: S = Q K^T (K-major operands), O += P V
 //                    with P from TMEM and V read along tokens (MN-major), so V
 //                    needs no transpose
+//   warp 17          looks pages and scales up, four tiles at a time, up to eight ahead
 // TMEM (512 columns): S0, S1 (128 each, P over the first 64), O0, O1 (D each).
+//
+// A softmax thread reads its 128 scores twice, 16 at a time (a maximum, then the
+// weights): that costs TMEM reads, which are idle otherwise, and saves the registers
+// that let eight converter warps run beside it.
 //
 // Block scales never touch the tiles: keys' are factors of the scores, values' join
 // the exponent (weights are 2^(z + lg)), and the weights' sum takes them out again.
@@ -33,14 +38,12 @@ namespace {
 
 constexpr int kRows = 256;     // rows an item
 constexpr int kTile = 128;     // tokens a tile
-constexpr int kThreads = 512;
+constexpr int kSoftmaxWarps = 8, kConvertWarps = 8, kIssueWarp = 16, kLookupWarp = 17;
+constexpr int kThreads = 32 * 18;
 constexpr int kTmemCols = 512;
-constexpr int kMeta = 4;       // ring of per-tile scales
-
-// Registers a thread by role: the block starts with kThreads * kRegsLaunch and the
-// shares must not sum to more (a share that cannot be had would wait forever).
-constexpr int kRegsLaunch = 128, kRegsSoftmax = 176, kRegsConvert = 104, kRegsIssue = 48;
-static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsConvert + 128 * kRegsIssue <= kThreads * kRegsLaunch, "");
+constexpr int kMeta = 8;       // ring of per-tile lookups
+constexpr int kMetaBatch = 4;  // tiles looked up at once
+constexpr int kChunks = kTile / 16;
 
 struct PrefillArgs {
     KvAttn a;
@@ -53,32 +56,38 @@ struct PrefillArgs {
     float* part_lse;  // [rows * Hq][splits]
 };
 
-struct TileScales {  // of 16 tokens
+struct ChunkScales {  // of 16 tokens
     float ks;   // negative: not seen
     float lg, inv;
     float pad;
 };
 
-__device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, uint32_t* v) {
+__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&v)[16]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];"
         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
-          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
-          "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
-          "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
         : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t* v) {
+// The loads before it are complete; tied to the registers so that no use moves ahead of it.
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&v)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                   "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st_x8_async(uint32_t taddr, const uint32_t (&v)[8]) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
-        "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
-        "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(v[0]),
+        "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
         : "memory");
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
 }
 // fp16 operands, fp32 accumulator; b_mn: B is read along N (MN-major).
 __host__ __device__ constexpr uint32_t idesc_f16(int m, int n, int b_mn) {
@@ -113,14 +122,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
     uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     uint8_t* q_smem = smem;                      // [2][kSub]
     uint8_t* ring = smem + 2 * L::kSub;          // [4][kSub]
-    __shared__ __align__(8) uint64_t full[4], empty[4], q_full[2], s_full[2], p_full[2], o_full[2], m_full[kMeta];
-    __shared__ TileScales scales[kMeta][kTile / 16];
+    __shared__ __align__(8) uint64_t full[4], empty[4], q_full[2], s_full[2], p_full[2], o_full[2],
+        m_full[kMeta], m_empty[kMeta];
+    __shared__ ChunkScales scales[kMeta][kChunks];
+    __shared__ int64_t places[kMeta][kChunks];  // byte offset of the chunk's codes of this head, -1: none
     __shared__ uint32_t tmem_slot, vmax_bits;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
     if (tid == 0) {
         for (int i = 0; i < 4; ++i) {
-            mbar_init(&full[i], 128);
+            mbar_init(&full[i], 32 * kConvertWarps);
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -129,7 +140,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
             mbar_init(&p_full[i], 128);
             mbar_init(&o_full[i], 1);
         }
-        for (int i = 0; i < kMeta; ++i) mbar_init(&m_full[i], 1);
+        for (int i = 0; i < kMeta; ++i) {
+            mbar_init(&m_full[i], 1);
+            mbar_init(&m_empty[i], kSoftmaxWarps + kConvertWarps);
+        }
         mbar_init_fence();
         vmax_bits = 0;
     }
@@ -176,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
         const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(most));
         if (lane == 0 && bits) atomicMax(&vmax_bits, bits);
     }
-    if (warp == 12) {
+    if (warp == kIssueWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)),
                      "r"(kTmemCols));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -188,9 +202,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
     const float vmax = __uint_as_float(vmax_bits);
     bool ok = true;
 
-    if (warp < 8) {
+    if (warp < kSoftmaxWarps) {
         // ------------------------------------------------------------- softmax
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
         const int sub = warp >> 2;
         const int r_sub = tid & 127;              // row of the subtile = TMEM lane
         const int row = sub * 128 + r_sub;
@@ -203,9 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
         bool bad = false;
         int64_t out_row = 0;
         {
-            uint4 raw[D / 8];
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i) raw[i] = make_uint4(0, 0, 0, 0);
+            const uint4* q = nullptr;
             if (row < rows) {
                 const int pos = span.first + tok;
                 if (p.a.causal) {
@@ -214,15 +225,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
                 }
                 const int hq = h * G + f % G;
                 out_row = (span.row0 + tok) * p.a.Hq + hq;
-                const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.a.q) +
-                                                                (span.row0 + tok) * p.a.q_stride + static_cast<int64_t>(hq) * D);
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i) raw[i] = __ldg(q + i);
+                q = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.a.q) +
+                                                   (span.row0 + tok) * p.a.q_stride + static_cast<int64_t>(hq) * D);
             }
             uint32_t most = 0;
-#pragma unroll
+#pragma unroll 8
             for (int i = 0; i < D / 8; ++i) {
-                const uint32_t u[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+                const uint4 r = q ? __ldg(q + i) : make_uint4(0, 0, 0, 0);
+                const uint32_t u[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) most = max(most, max((u[j] << 16) & 0x7FFFFFFFu, u[j] & 0x7FFF0000u));
             }
@@ -231,9 +241,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
             // a negative scale goes into the queries: scores times zc keep their order
             const float down = p.a.scale < 0.f ? -pow2_bits(254u - ex) : pow2_bits(254u - ex);
             zc = fabsf(p.a.scale) * kLog2e * pow2_bits(ex);
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-                const uint32_t u[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll 8
+            for (int i = 0; i < D / 8; ++i) {  // the second time from the L1
+                const uint4 r = q ? __ldg(q + i) : make_uint4(0, 0, 0, 0);
+                const uint32_t u[4] = {r.x, r.y, r.z, r.w};
                 uint32_t x[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
@@ -247,47 +258,35 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
         float ref = -INFINITY, l = 0.f;
         for (int i = 0; ok && i < tiles; ++i) {
             const int j0 = lo + i * kTile;
-            ok = mbar_wait(&m_full[i & (kMeta - 1)], (i / kMeta) & 1, 0x71) && mbar_wait(&s_full[sub], i & 1, 0x72);
+            const int ms = i & (kMeta - 1);
+            ok = mbar_wait(&m_full[ms], (i / kMeta) & 1, 0x71) && mbar_wait(&s_full[sub], i & 1, 0x72);
             if (!ok) break;
             tc::tc_fence_after();
-            uint32_t sr[128];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld_x32(s_at + 32u * c, sr + 32 * c);
-            tmem_ld_wait();
-            const TileScales* ts = scales[i & (kMeta - 1)];
-            float k[8];
+            const ChunkScales* ts = scales[ms];
+            // does every row of the warp see all of the tile?
             bool all = row_lo <= j0 && row_hi >= j0 + kTile;
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                k[c] = ts[c].ks;
-                all &= k[c] >= 0.f;
-                k[c] *= zc;
-            }
+            all &= ts[lane & (kChunks - 1)].ks >= 0.f;
+            const bool whole = __all_sync(0xffffffffu, all);
+            uint32_t sv[2][16];
             float mx = -INFINITY;
-            if (__all_sync(0xffffffffu, all)) {
+            tmem_ld_x16(s_at, sv[0]);
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    float m = __uint_as_float(sr[16 * c]);
-#pragma unroll
-                    for (int e = 1; e < 16; ++e) m = fmaxf(m, __uint_as_float(sr[16 * c + e]));
-                    mx = fmaxf(mx, fmaf(m, k[c], ts[c].lg));
-                }
-            } else {  // some rows of the warp do not see all of the tile
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const bool seen = ts[c].ks >= 0.f;
-                    float m = -INFINITY;
+            for (int c = 0; c < kChunks; ++c) {
+                uint32_t(&v)[16] = sv[c & 1];
+                tmem_ld_wait(v);
+                tmem_ld_x16(s_at + 16u * ((c + 1) & (kChunks - 1)), sv[(c + 1) & 1]);  // the last: the first again
+                const ChunkScales t = ts[c];
+                if (!whole) {
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         const int j = j0 + 16 * c + e;
-                        float z = __uint_as_float(sr[16 * c + e]) * k[c];
-                        if (!seen || j < row_lo || j >= row_hi) z = -INFINITY;
-                        sr[16 * c + e] = __float_as_uint(z);
-                        m = fmaxf(m, z);
+                        if (t.ks < 0.f || j < row_lo || j >= row_hi) v[e] = 0xFF800000u;
                     }
-                    k[c] = 1.f;
-                    mx = fmaxf(mx, m + ts[c].lg);
                 }
+                float m = __uint_as_float(v[0]);
+#pragma unroll
+                for (int e = 1; e < 16; ++e) m = fmaxf(m, __uint_as_float(v[e]));
+                if (m > -INFINITY) mx = fmaxf(mx, fmaf(m, zc * t.ks, t.lg));
             }
             const bool up = mx > ref + kSlack;
             if (__any_sync(0xffffffffu, up)) {
@@ -296,17 +295,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
                 ref = up ? mx : ref;
                 l *= fct;
                 if (i > 0) {
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < D / 16; ++c) {
                         uint32_t ov[16];
-                        asm volatile(
-                            "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-                            "%12, %13, %14, %15}, [%16];"
-                            : "=r"(ov[0]), "=r"(ov[1]), "=r"(ov[2]), "=r"(ov[3]), "=r"(ov[4]), "=r"(ov[5]), "=r"(ov[6]),
-                              "=r"(ov[7]), "=r"(ov[8]), "=r"(ov[9]), "=r"(ov[10]), "=r"(ov[11]), "=r"(ov[12]),
-                              "=r"(ov[13]), "=r"(ov[14]), "=r"(ov[15])
-                            : "r"(o_at + 16u * c));
-                        tmem_ld_wait();
+                        tmem_ld_x16(o_at + 16u * c, ov);
+                        tmem_ld_wait(ov);
 #pragma unroll
                         for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * fct);
                         tc::tmem_st_x16_async(o_at + 16u * c, ov);
@@ -315,25 +308,37 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
                 }
             }
             const float minus_ref = kLift - (ref > -INFINITY ? ref : 0.f);
-            uint32_t pw[64];
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                const float base = ts[c].lg + minus_ref;
-                float sum = 0.f;
+            for (int c = 0; c < kChunks; ++c) {
+                uint32_t(&v)[16] = sv[c & 1];
+                tmem_ld_wait(v);
+                if (c + 1 < kChunks) tmem_ld_x16(s_at + 16u * (c + 1), sv[(c + 1) & 1]);
+                const ChunkScales t = ts[c];
+                const uint32_t k1 = __float_as_uint(zc * t.ks), b1 = __float_as_uint(t.lg + minus_ref);
+                const uint64_t k2 = tc::f2_pack(k1, k1), b2 = tc::f2_pack(b1, b1);
+                uint64_t sum = 0;
+                uint32_t pw[8];
 #pragma unroll
                 for (int e = 0; e < 16; e += 2) {
-                    const float w0 = exp2_approx(fmaf(__uint_as_float(sr[16 * c + e]), k[c], base));
-                    const float w1 = exp2_approx(fmaf(__uint_as_float(sr[16 * c + e + 1]), k[c], base));
-                    sum += w0 + w1;
-                    pw[8 * c + e / 2] = f2_to_h2(w0, w1);
+                    const uint64_t z = tc::f2_fma(tc::f2_pack(v[e], v[e + 1]), k2, b2);
+                    float w0 = exp2_approx(__uint_as_float(static_cast<uint32_t>(z)));
+                    float w1 = exp2_approx(__uint_as_float(static_cast<uint32_t>(z >> 32)));
+                    if (!whole) {
+                        const int j = j0 + 16 * c + e;
+                        w0 = t.ks < 0.f || j < row_lo || j >= row_hi ? 0.f : w0;
+                        w1 = t.ks < 0.f || j + 1 < row_lo || j + 1 >= row_hi ? 0.f : w1;
+                    }
+                    sum = f2_add(sum, tc::f2_pack(__float_as_uint(w0), __float_as_uint(w1)));
+                    pw[e / 2] = f2_to_h2(w0, w1);
                 }
-                l = fmaf(sum, ts[c].inv, l);
+                l = fmaf(__uint_as_float(static_cast<uint32_t>(sum)) + __uint_as_float(static_cast<uint32_t>(sum >> 32)), t.inv, l);
+                tmem_st_x8_async(s_at + 8u * c, pw);  // over scores that are read
             }
-            tmem_st_x32(s_at, pw);
-            tmem_st_x32(s_at + 32u, pw + 32);
             tc::tmem_st_wait();
             tc::tc_fence_before();
             mbar_arrive(&p_full[sub]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&m_empty[ms]);
         }
         // ---- output
         if (ok && tiles > 0) ok = mbar_wait(&o_full[sub], 0, 0x73);
@@ -342,27 +347,27 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
             const bool live = row < rows;
             const float inv = bad ? NAN : l > 0.f || l != l ? vmax / l : 0.f;
             const int64_t at = p.splits > 1 ? out_row * p.splits + blockIdx.y : 0;
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-                uint32_t ov[32];
+#pragma unroll 2
+            for (int c = 0; c < D / 16; ++c) {
+                uint32_t ov[16];
                 if (tiles > 0) {
-                    tmem_ld_x32(o_at + 32u * c, ov);
-                    tmem_ld_wait();
+                    tmem_ld_x16(o_at + 16u * c, ov);
+                    tmem_ld_wait(ov);
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) ov[e] = 0;
+                    for (int e = 0; e < 16; ++e) ov[e] = 0;
                 }
                 if (!live) continue;
                 if (p.splits > 1) {
-                    float4* o = reinterpret_cast<float4*>(p.part_o + at * D + 32 * c);
+                    float4* o = reinterpret_cast<float4*>(p.part_o + at * D + 16 * c);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
+                    for (int e = 0; e < 4; ++e)
                         o[e] = make_float4(__uint_as_float(ov[4 * e]) * inv, __uint_as_float(ov[4 * e + 1]) * inv,
                                            __uint_as_float(ov[4 * e + 2]) * inv, __uint_as_float(ov[4 * e + 3]) * inv);
                 } else {
-                    uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.a.out) + out_row * D + 32 * c);
+                    uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.a.out) + out_row * D + 16 * c);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
+                    for (int e = 0; e < 2; ++e) {
                         uint32_t x[4];
 #pragma unroll
                         for (int n = 0; n < 4; ++n)
@@ -375,36 +380,28 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
                 p.part_lse[at] = bad || l != l ? 0.f : l > 0.f ? ref - kLift + log2f(l) : -INFINITY;
         }
         tc::tc_fence_before();
-    } else if (warp < 12) {
+    } else if (warp < kSoftmaxWarps + kConvertWarps) {
         // ---------------------------------------------------------- converters
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConvert));
-        const int ct = tid - 256;
-        constexpr int kVecs = D / 16;                 // 16-byte pieces of codes a token
-        constexpr int kStep = 128 / kVecs;            // tokens a pass of the 128 threads
-        constexpr int kPasses = kTile / kStep;        // 8 (D 128) or 4 (D 64)
+        const int ct = tid - 32 * kSoftmaxWarps;
+        constexpr int kVecs = D / 16;                        // 16-byte pieces of codes a token
+        constexpr int kStep = 32 * kConvertWarps / kVecs;    // tokens a pass of all threads
+        constexpr int kPasses = kTile / kStep;               // 4 (D 128) or 2 (D 64)
         const int vec = ct % kVecs, tok0 = ct / kVecs;
-        // byte offset of (token tok0 + kStep n) in the tile's codes, by pass; -1: nothing there
-        int64_t at[kPasses];
-        auto places = [&](int i) {
-            const int j0 = lo + i * kTile;
+        // threads of the two halves of 64 values store their two pieces in opposite order: no bank conflicts
+        const int swap = (vec >> 2) & 1;
+        auto load = [&](const uint8_t* codes, int i, uint4 (&raw)[kPasses]) {
+            const int64_t* at = places[i & (kMeta - 1)];
+            const int left = hi - (lo + i * kTile);
 #pragma unroll
             for (int n = 0; n < kPasses; ++n) {
-                const int j = j0 + tok0 + kStep * n;
-                at[n] = -1;
-                if (j < hi) {
-                    const int b = j / p.c.block;
-                    const int32_t page = __ldg(p.st.pages + static_cast<int64_t>(s) * p.st.max_pages + b);
-                    if (page >= 0 && page < p.c.P)
-                        at[n] = ((static_cast<int64_t>(page) * p.c.H + h) * p.c.block + (j - b * p.c.block)) * D + 16 * vec;
-                }
+                const int r = tok0 + kStep * n;
+                const int64_t o = at[r >> 4];
+                raw[n] = make_uint4(0, 0, 0, 0);
+                if (o >= 0 && r < left) raw[n] = __ldg(reinterpret_cast<const uint4*>(codes + o + ((r & 15) * D + 16 * vec)));
             }
         };
-        auto load = [&](const uint8_t* codes, uint4 (&raw)[kPasses]) {
-#pragma unroll
-            for (int n = 0; n < kPasses; ++n)
-                raw[n] = at[n] >= 0 ? __ldg(reinterpret_cast<const uint4*>(codes + at[n])) : make_uint4(0, 0, 0, 0);
-        };
         auto convert = [&](const uint4 (&raw)[kPasses], uint8_t* tile) {
+            uint8_t* half = tile + (vec >> 2) * L::kHalf;
 #pragma unroll
             for (int n = 0; n < kPasses; ++n) {
                 const uint32_t x[4] = {raw[n].x, raw[n].y, raw[n].z, raw[n].w};
@@ -415,9 +412,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
                     y[m] = make_uint4(pair_lo_h2<MODE>(a), pair_hi_h2<MODE>(a), pair_lo_h2<MODE>(b), pair_hi_h2<MODE>(b));
                 }
                 const int r = tok0 + kStep * n;
-                uint8_t* half = tile + (vec >> 2) * L::kHalf;
-                // threads of the two halves store their two pieces in opposite order: no bank conflicts
-                const int swap = (vec >> 2) & 1;
                 *reinterpret_cast<uint4*>(half + sw128_at(r, 2 * (vec & 3) + swap)) = swap ? y[1] : y[0];
                 *reinterpret_cast<uint4*>(half + sw128_at(r, 2 * (vec & 3) + 1 - swap)) = swap ? y[0] : y[1];
             }
@@ -425,48 +419,61 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
         };
         uint4 kraw[kPasses], vraw[kPasses];
         if (tiles > 0) {
-            places(0);
-            load(p.c.k_codes, kraw);
+            ok = mbar_wait(&m_full[0], 0, 0x74);
+            if (ok) load(p.c.k_codes, 0, kraw);
         }
         for (int i = 0; ok && i < tiles; ++i) {
-            load(p.c.v_codes, vraw);
-            if (ct < kTile / 16) {  // scales of 16 tokens each
-                const int j = lo + i * kTile + 16 * ct;
-                TileScales t{-1.f, 0.f, 1.f, 0.f};
-                if (j < hi) {
-                    const int page = page_of(p.st, p.c, s, j / p.c.block);
-                    if (page >= 0) {
-                        const int64_t ph = static_cast<int64_t>(page) * p.c.H + h;
-                        const float vs = __ldg(p.c.v_scales + ph);
-                        t.ks = __ldg(p.c.k_scales + ph);
-                        t.lg = vs > 0.f ? fmaxf(log2f(vs) - log2f(vmax), kLgMin) : kLgMin;
-                        t.inv = exp2f(-t.lg);
-                    }
-                }
-                scales[i & (kMeta - 1)][ct] = t;
-            }
-            if (warp == 8) {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&m_full[i & (kMeta - 1)]);
-            }
+            load(p.c.v_codes, i, vraw);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&m_empty[i & (kMeta - 1)]);
             const int ks = 2 * (i & 1), vs = ks + 1;
             const uint32_t free_parity = ((i >> 1) & 1) ^ 1;
-            ok = mbar_wait(&empty[ks], free_parity, 0x74);
+            ok = mbar_wait(&empty[ks], free_parity, 0x75);
             if (!ok) break;
             convert(kraw, ring + ks * L::kSub);
             mbar_arrive(&full[ks]);
             if (i + 1 < tiles) {
-                places(i + 1);
-                load(p.c.k_codes, kraw);
+                ok = mbar_wait(&m_full[(i + 1) & (kMeta - 1)], ((i + 1) / kMeta) & 1, 0x7B);
+                if (!ok) break;
+                load(p.c.k_codes, i + 1, kraw);
             }
-            ok = mbar_wait(&empty[vs], free_parity, 0x75);
+            ok = mbar_wait(&empty[vs], free_parity, 0x7C);
             if (!ok) break;
             convert(vraw, ring + vs * L::kSub);
             mbar_arrive(&full[vs]);
         }
+    } else if (warp == kLookupWarp) {
+        // ------------------------------------------------- pages and scales: lane = (tile of four, chunk of 16 tokens)
+        const float lg_max = log2f(vmax);
+        for (int i0 = 0; ok && i0 < tiles; i0 += kMetaBatch) {
+            const int i = i0 + lane / kChunks, c = lane % kChunks;
+            const int j = lo + i * kTile + 16 * c;
+            ChunkScales t{-1.f, 0.f, 1.f, 0.f};
+            int64_t at = -1;
+            if (i < tiles && j < hi) {
+                const int b = j / p.c.block;
+                const int page = page_of(p.st, p.c, s, b);
+                if (page >= 0) {
+                    const int64_t ph = static_cast<int64_t>(page) * p.c.H + h;
+                    const float vs = __ldg(p.c.v_scales + ph);
+                    at = (ph * p.c.block + (j - b * p.c.block)) * D;
+                    t.ks = __ldg(p.c.k_scales + ph);
+                    t.lg = vs > 0.f ? fmaxf(log2f(vs) - lg_max, kLgMin) : kLgMin;
+                    t.inv = exp2f(-t.lg);
+                }
+            }
+            for (int n = i0; ok && n < i0 + kMetaBatch && n < tiles; ++n)
+                ok = mbar_wait(&m_empty[n & (kMeta - 1)], ((n / kMeta) & 1) ^ 1, 0x7D);
+            if (!ok) break;
+            if (i < tiles) {
+                scales[i & (kMeta - 1)][c] = t;
+                places[i & (kMeta - 1)][c] = at;
+            }
+            __syncwarp();
+            if (i < tiles && c == 0) mbar_arrive(&m_full[i & (kMeta - 1)]);
+        }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
-        if (warp == 12 && lane == 0 && tiles > 0) {
+        if (lane == 0 && tiles > 0) {
             // ------------------------------------------------------ the products
             constexpr uint32_t idesc_s = idesc_f16(128, kTile, 0), idesc_o = idesc_f16(128, D, 1);
             auto qk = [&](int sub, int i) {
@@ -519,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
         __syncwarp();
     }
     __syncthreads();
-    if (warp == 12) {
+    if (warp == kIssueWarp) {
         tc::tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
     }
@@ -566,12 +573,6 @@ cudaError_t launch(const PrefillArgs& p, cudaStream_t stream) {
     cudaError_t e = cudaFuncSetAttribute(kv_attn_prefill_kernel<MODE, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          Smem<D>::kBytes);
     if (e != cudaSuccess) return e;
-    // the register shares are taken from what the block is launched with
-    static const int regs = [] {
-        cudaFuncAttributes at{};
-        return cudaFuncGetAttributes(&at, kv_attn_prefill_kernel<MODE, D>) == cudaSuccess ? at.numRegs : 0;
-    }();
-    if (regs < kRegsLaunch) return cudaErrorLaunchOutOfResources;
     cudaLaunchAttribute pdl[1];
     pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     pdl[0].val.programmaticStreamSerializationAllowed = 1;
