@@ -6,21 +6,19 @@
 // SM and item; rows form two subtiles of 128 that share every converted key and
 // value tile and take turns on the tensor core: while one subtile's softmax runs, the
 // other's products do.
-//   warps 0-3, 4-7   softmax of subtile 0, 1: thread = row = TMEM lane; scores
+//   warp 0           issues the products (the lowest warp: it goes before the others
+//                    when it has an instruction ready): S = Q K^T (K-major operands), O += P V
+//                    with P from TMEM and V read along tokens (MN-major), so V
+//                    needs no transpose
+//   warp 1           looks pages and scales up, four tiles at a time, up to eight ahead
+//   warps 2, 3       fill the warpgroup (registers are dealt out by warpgroups)
+//   warps 4-7, 8-11  softmax of subtile 0, 1: thread = row = TMEM lane; scores
 //                    arrive in TMEM, weights go back over them as fp16
-//   warps 8-15       converters: 8-bit codes from global memory (the next tile's
+//   warps 12-19      converters: 8-bit codes from global memory (the next tile's
 //                    loads are in flight while this one's are converted), exact
 //                    fp16 into swizzled shared tiles [token][value], a ring of two
 //                    K and two V tiles
-//   warp 16          issues the products: S = Q K^T (K-major operands), O += P V
-//                    with P from TMEM and V read along tokens (MN-major), so V
-//                    needs no transpose
-//   warp 17          looks pages and scales up, four tiles at a time, up to eight ahead
 // TMEM (512 columns): S0, S1 (128 each, P over the first 64), O0, O1 (D each).
-//
-// A softmax thread reads its 128 scores twice, 16 at a time (a maximum, then the
-// weights): that costs TMEM reads, which are idle otherwise, and saves the registers
-// that let eight converter warps run beside it.
 //
 // Block scales never touch the tiles: keys' are factors of the scores, values' join
 // the exponent (weights are 2^(z + lg)), and the weights' sum takes them out again.
@@ -38,8 +36,12 @@ namespace {
 
 constexpr int kRows = 256;     // rows an item
 constexpr int kTile = 128;     // tokens a tile
-constexpr int kSoftmaxWarps = 8, kConvertWarps = 8, kIssueWarp = 16, kLookupWarp = 17;
-constexpr int kThreads = 32 * 18;
+constexpr int kIssueWarp = 0, kLookupWarp = 1, kSoftmaxWarp0 = 4, kSoftmaxWarps = 8, kConvertWarp0 = 12, kConvertWarps = 8;
+constexpr int kThreads = 32 * 20;
+// Registers a thread by role: the block starts with kThreads * kRegsLaunch, and the
+// shares must not sum to more (a share that cannot be had would wait forever).
+constexpr int kRegsLaunch = 96, kRegsSoftmax = 136, kRegsConvert = 88, kRegsRest = 32;
+static_assert(32 * kSoftmaxWarps * kRegsSoftmax + 32 * kConvertWarps * kRegsConvert + 128 * kRegsRest <= kThreads * kRegsLaunch, "");
 constexpr int kTmemCols = 512;
 constexpr int kMeta = 8;       // ring of per-tile lookups
 constexpr int kMetaBatch = 4;  // tiles looked up at once
@@ -104,6 +106,17 @@ __device__ __forceinline__ uint64_t sw128_mn_desc(const void* p, uint32_t lead) 
 // Byte offset of 16-byte piece `piece` (8 values) of row r in a [rows][64 values] swizzled tile.
 __device__ __forceinline__ uint32_t sw128_at(int r, int piece) {
     return static_cast<uint32_t>((r >> 3) * 1024 + (r & 7) * 128 + ((piece ^ (r & 7)) << 4));
+}
+
+// What a 16-token chunk's scores are multiplied by: positive even where keys or
+// queries are all zero, so that a score of -infinity (not seen) stays one.
+__device__ __forceinline__ float score_factor(float zc, float ks) { return fmaxf(zc * ks, 1e-37f); }
+
+// Scores outside [from, to) of a chunk become -infinity.
+__device__ __forceinline__ void hide(uint32_t (&v)[16], int from, int to) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+        if (e < from || e >= to) v[e] = 0xFF800000u;
 }
 
 template <int D>
@@ -202,9 +215,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
     const float vmax = __uint_as_float(vmax_bits);
     bool ok = true;
 
-    if (warp < kSoftmaxWarps) {
+    if (warp >= kSoftmaxWarp0 && warp < kSoftmaxWarp0 + kSoftmaxWarps) {
         // ------------------------------------------------------------- softmax
-        const int sub = warp >> 2;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+        const int sub = (warp - kSoftmaxWarp0) >> 2;
         const int r_sub = tid & 127;              // row of the subtile = TMEM lane
         const int row = sub * 128 + r_sub;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -267,26 +281,37 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
             bool all = row_lo <= j0 && row_hi >= j0 + kTile;
             all &= ts[lane & (kChunks - 1)].ks >= 0.f;
             const bool whole = __all_sync(0xffffffffu, all);
-            uint32_t sv[2][16];
-            float mx = -INFINITY;
+            const int from = row_lo - j0, to = row_hi - j0;
+            // Scores are read twice, 32 at a time with the next 32 in flight, in rolled loops: the code of
+            // the three roles has to stay in the instruction caches (unrolled, the warps waited for
+            // instructions more than for anything else).
+            uint32_t sv[4][16];
             tmem_ld_x16(s_at, sv[0]);
-#pragma unroll
-            for (int c = 0; c < kChunks; ++c) {
-                uint32_t(&v)[16] = sv[c & 1];
-                tmem_ld_wait(v);
-                tmem_ld_x16(s_at + 16u * ((c + 1) & (kChunks - 1)), sv[(c + 1) & 1]);  // the last: the first again
+            tmem_ld_x16(s_at + 16u, sv[1]);
+            float mx = -INFINITY;
+            auto largest = [&](uint32_t (&v)[16], int c) {
                 const ChunkScales t = ts[c];
-                if (!whole) {
+                if (!whole) hide(v, t.ks >= 0.f ? from - 16 * c : 16, to - 16 * c);
+                float m[2] = {__uint_as_float(v[0]), __uint_as_float(v[1])};
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const int j = j0 + 16 * c + e;
-                        if (t.ks < 0.f || j < row_lo || j >= row_hi) v[e] = 0xFF800000u;
-                    }
-                }
-                float m = __uint_as_float(v[0]);
-#pragma unroll
-                for (int e = 1; e < 16; ++e) m = fmaxf(m, __uint_as_float(v[e]));
-                if (m > -INFINITY) mx = fmaxf(mx, fmaf(m, zc * t.ks, t.lg));
+                for (int e = 2; e < 16; ++e) m[e & 1] = fmaxf(m[e & 1], __uint_as_float(v[e]));
+                mx = fmaxf(mx, fmaf(fmaxf(m[0], m[1]), score_factor(zc, t.ks), t.lg));
+            };
+#pragma unroll 1
+            for (int c = 0; c < kChunks; c += 4) {
+                tmem_ld_wait(sv[0]);
+                tmem_ld_wait(sv[1]);
+                tmem_ld_x16(s_at + 16u * (c + 2), sv[2]);
+                tmem_ld_x16(s_at + 16u * (c + 3), sv[3]);
+                largest(sv[0], c);
+                largest(sv[1], c + 1);
+                tmem_ld_wait(sv[2]);
+                tmem_ld_wait(sv[3]);
+                const uint32_t next = s_at + 16u * ((c + 4) & (kChunks - 1));  // behind the last: the first again
+                tmem_ld_x16(next, sv[0]);
+                tmem_ld_x16(next + 16u, sv[1]);
+                largest(sv[2], c + 2);
+                largest(sv[3], c + 3);
             }
             const bool up = mx > ref + kSlack;
             if (__any_sync(0xffffffffu, up)) {
@@ -308,31 +333,40 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
                 }
             }
             const float minus_ref = kLift - (ref > -INFINITY ? ref : 0.f);
-#pragma unroll
-            for (int c = 0; c < kChunks; ++c) {
-                uint32_t(&v)[16] = sv[c & 1];
-                tmem_ld_wait(v);
-                if (c + 1 < kChunks) tmem_ld_x16(s_at + 16u * (c + 1), sv[(c + 1) & 1]);
+            auto weigh = [&](uint32_t (&v)[16], int c) {  // chunk c's weights, as fp16 over scores that are done
                 const ChunkScales t = ts[c];
-                const uint32_t k1 = __float_as_uint(zc * t.ks), b1 = __float_as_uint(t.lg + minus_ref);
+                if (!whole) hide(v, t.ks >= 0.f ? from - 16 * c : 16, to - 16 * c);
+                const uint32_t k1 = __float_as_uint(score_factor(zc, t.ks)), b1 = __float_as_uint(t.lg + minus_ref);
                 const uint64_t k2 = tc::f2_pack(k1, k1), b2 = tc::f2_pack(b1, b1);
                 uint64_t sum = 0;
                 uint32_t pw[8];
 #pragma unroll
                 for (int e = 0; e < 16; e += 2) {
                     const uint64_t z = tc::f2_fma(tc::f2_pack(v[e], v[e + 1]), k2, b2);
-                    float w0 = exp2_approx(__uint_as_float(static_cast<uint32_t>(z)));
-                    float w1 = exp2_approx(__uint_as_float(static_cast<uint32_t>(z >> 32)));
-                    if (!whole) {
-                        const int j = j0 + 16 * c + e;
-                        w0 = t.ks < 0.f || j < row_lo || j >= row_hi ? 0.f : w0;
-                        w1 = t.ks < 0.f || j + 1 < row_lo || j + 1 >= row_hi ? 0.f : w1;
-                    }
+                    const float w0 = exp2_approx(__uint_as_float(static_cast<uint32_t>(z)));
+                    const float w1 = exp2_approx(__uint_as_float(static_cast<uint32_t>(z >> 32)));
                     sum = f2_add(sum, tc::f2_pack(__float_as_uint(w0), __float_as_uint(w1)));
                     pw[e / 2] = f2_to_h2(w0, w1);
                 }
                 l = fmaf(__uint_as_float(static_cast<uint32_t>(sum)) + __uint_as_float(static_cast<uint32_t>(sum >> 32)), t.inv, l);
-                tmem_st_x8_async(s_at + 8u * c, pw);  // over scores that are read
+                tmem_st_x8_async(s_at + 8u * c, pw);
+            };
+#pragma unroll 1
+            for (int c = 0; c < kChunks; c += 4) {
+                tmem_ld_wait(sv[0]);
+                tmem_ld_wait(sv[1]);
+                tmem_ld_x16(s_at + 16u * (c + 2), sv[2]);
+                tmem_ld_x16(s_at + 16u * (c + 3), sv[3]);
+                weigh(sv[0], c);
+                weigh(sv[1], c + 1);
+                tmem_ld_wait(sv[2]);
+                tmem_ld_wait(sv[3]);
+                if (c + 4 < kChunks) {
+                    tmem_ld_x16(s_at + 16u * (c + 4), sv[0]);
+                    tmem_ld_x16(s_at + 16u * (c + 5), sv[1]);
+                }
+                weigh(sv[2], c + 2);
+                weigh(sv[3], c + 3);
             }
             tc::tmem_st_wait();
             tc::tc_fence_before();
@@ -380,9 +414,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
                 p.part_lse[at] = bad || l != l ? 0.f : l > 0.f ? ref - kLift + log2f(l) : -INFINITY;
         }
         tc::tc_fence_before();
-    } else if (warp < kSoftmaxWarps + kConvertWarps) {
+    } else if (warp >= kConvertWarp0) {
         // ---------------------------------------------------------- converters
-        const int ct = tid - 32 * kSoftmaxWarps;
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConvert));
+        const int ct = tid - 32 * kConvertWarp0;
         constexpr int kVecs = D / 16;                        // 16-byte pieces of codes a token
         constexpr int kStep = 32 * kConvertWarps / kVecs;    // tokens a pass of all threads
         constexpr int kPasses = kTile / kStep;               // 4 (D 128) or 2 (D 64)
@@ -442,7 +477,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
             convert(vraw, ring + vs * L::kSub);
             mbar_arrive(&full[vs]);
         }
-    } else if (warp == kLookupWarp) {
+    } else {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+      if (warp == kLookupWarp) {
         // ------------------------------------------------- pages and scales: lane = (tile of four, chunk of 16 tokens)
         const float lg_max = log2f(vmax);
         for (int i0 = 0; ok && i0 < tiles; i0 += kMetaBatch) {
@@ -472,24 +509,29 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
             __syncwarp();
             if (i < tiles && c == 0) mbar_arrive(&m_full[i & (kMeta - 1)]);
         }
-    } else {
+      } else if (warp == kIssueWarp) {
         if (lane == 0 && tiles > 0) {
             // ------------------------------------------------------ the products
             constexpr uint32_t idesc_s = idesc_f16(128, kTile, 0), idesc_o = idesc_f16(128, D, 1);
+            // everything but the tile's ring slot (kSub apart) is fixed
+            const uint64_t q_desc = tc::sw128_desc(q_smem), k_desc = tc::sw128_desc(ring);
+            const uint64_t v_desc = sw128_mn_desc(ring + L::kSub, L::kHalf);
+            constexpr uint64_t kSubUnits = L::kSub >> 4;
             auto qk = [&](int sub, int i) {
-                const uint64_t a = tc::sw128_desc(q_smem + sub * L::kSub), b = tc::sw128_desc(ring + 2 * (i & 1) * L::kSub);
-#pragma unroll
+                const uint64_t a = q_desc + (sub ? kSubUnits : 0), b = k_desc + (i & 1 ? 2 * kSubUnits : 0);
+                const uint32_t d = tmem + sub * 128;
+#pragma unroll 2
                 for (int k = 0; k < D / 16; ++k) {
-                    const uint64_t off = static_cast<uint64_t>(((k >> 2) * L::kHalf + (k & 3) * 32) >> 4);
-                    tc::tc_mma(tmem + sub * 128, a + off, b + off, idesc_s, k > 0);
+                    constexpr uint64_t kHalfUnits = L::kHalf >> 4;
+                    const uint64_t off = (k >> 2) * kHalfUnits + (k & 3) * 2;
+                    tc::tc_mma(d, a + off, b + off, idesc_s, k > 0);
                 }
             };
             auto pv = [&](int sub, int i) {
-                const uint64_t b = sw128_mn_desc(ring + (2 * (i & 1) + 1) * L::kSub, L::kHalf);
-#pragma unroll
-                for (int k = 0; k < kTile / 16; ++k)
-                    tc::tc_mma_ts(tmem + 256 + sub * D, tmem + sub * 128 + 8 * k, b + static_cast<uint64_t>(k * 2048 >> 4), idesc_o,
-                                  i > 0 || k > 0);
+                const uint64_t b = v_desc + (i & 1 ? 2 * kSubUnits : 0);
+                const uint32_t d = tmem + 256 + sub * D, a = tmem + sub * 128;
+#pragma unroll 2
+                for (int k = 0; k < kTile / 16; ++k) tc::tc_mma_ts(d, a + 8 * k, b + k * 128, idesc_o, i > 0 || k > 0);
             };
             ok = mbar_wait(&full[0], 0, 0x76);
             for (int sub = 0; ok && sub < 2; ++sub) {
@@ -524,6 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
             }
         }
         __syncwarp();
+      }
     }
     __syncthreads();
     if (warp == kIssueWarp) {
@@ -573,6 +616,12 @@ cudaError_t launch(const PrefillArgs& p, cudaStream_t stream) {
     cudaError_t e = cudaFuncSetAttribute(kv_attn_prefill_kernel<MODE, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          Smem<D>::kBytes);
     if (e != cudaSuccess) return e;
+    // the register shares are taken from what the block is launched with
+    static const int regs = [] {
+        cudaFuncAttributes at{};
+        return cudaFuncGetAttributes(&at, kv_attn_prefill_kernel<MODE, D>) == cudaSuccess ? at.numRegs : 0;
+    }();
+    if (regs < kRegsLaunch) return cudaErrorLaunchOutOfResources;
     cudaLaunchAttribute pdl[1];
     pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     pdl[0].val.programmaticStreamSerializationAllowed = 1;
