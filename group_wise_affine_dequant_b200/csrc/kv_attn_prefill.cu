@@ -80,21 +80,67 @@ __device__ __forceinline__ void tmem_ld_wait(uint32_t (&v)[16]) {
                  :
                  : "memory");
 }
-__device__ __forceinline__ void tmem_st_x8_async(uint32_t taddr, const uint32_t (&v)[8]) {
+// No wait (tc::tmem_st_wait), and no claim on other memory: loads may move across.
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&v)[16]) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(v[0]),
-        "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-        : "memory");
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+        "%12, %13, %14, %15, %16};" ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]),
+        "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]));
 }
 __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
     uint64_t d;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// 2^z for two values on the FMA pipe (the special-function pipe, 16 results a clock and SM,
+// would be the limit with all of them): z = n + f, n the nearest integer (Cody and Waite's
+// reduction), 2^f on [-1/2, 1/2] by the cubic of least relative error (7.5e-5, 0.3 of an
+// fp16 rounding), n added to the exponent. z below -126 gives 2^-126, which fp16 rounds to 0.
+__device__ __forceinline__ uint64_t f2_exp2(uint64_t z) {
+    const float z0 = fmaxf(__uint_as_float(static_cast<uint32_t>(z)), -126.f);
+    const float z1 = fmaxf(__uint_as_float(static_cast<uint32_t>(z >> 32)), -126.f);
+    z = tc::f2_pack(__float_as_uint(z0), __float_as_uint(z1));
+    auto both = [](uint32_t c) { return tc::f2_pack(c, c); };
+    const uint64_t t = f2_add(z, both(0x4B400000u));                          // 1.5 * 2^23: n in the low bits
+    const uint64_t f = tc::f2_fma(f2_add(t, both(0xCB400000u)), both(0xBF800000u), z);
+    uint64_t p = tc::f2_fma(both(0x3D61FBB0u), f, both(0x3E786F0Du));         // 0.0551717, 0.242611
+    p = tc::f2_fma(p, f, both(0x3F31798Du));                                  // 0.693261
+    p = tc::f2_fma(p, f, both(0x3F7FFB49u));                                  // 0.999928
+    const uint32_t lo = static_cast<uint32_t>(p) + (static_cast<uint32_t>(t) << 23);
+    const uint32_t hi = static_cast<uint32_t>(p >> 32) + (static_cast<uint32_t>(t >> 32) << 23);
+    return tc::f2_pack(lo, hi);
+}
 // fp16 operands, fp32 accumulator; b_mn: B is read along N (MN-major).
 __host__ __device__ constexpr uint32_t idesc_f16(int m, int n, int b_mn) {
     return (1u << 4) | (static_cast<uint32_t>(b_mn) << 16) | (static_cast<uint32_t>(n >> 3) << 17) |
            (static_cast<uint32_t>(m >> 4) << 24);
+}
+// The products and commits of the issuing warp: all lanes go along (uniform addresses stay
+// in uniform registers), one elected lane issues.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+        "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
+        "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void commit_elected(uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
+        : "memory");
 }
 // MN-major, 128-byte swizzle: rows of 64 values; 8-token groups 1024 bytes apart
 // (stride offset), the next 64 values `lead` bytes on (leading offset).
@@ -111,13 +157,6 @@ __device__ __forceinline__ uint32_t sw128_at(int r, int piece) {
 // What a 16-token chunk's scores are multiplied by: positive even where keys or
 // queries are all zero, so that a score of -infinity (not seen) stays one.
 __device__ __forceinline__ float score_factor(float zc, float ks) { return fmaxf(zc * ks, 1e-37f); }
-
-// Scores outside [from, to) of a chunk become -infinity.
-__device__ __forceinline__ void hide(uint32_t (&v)[16], int from, int to) {
-#pragma unroll
-    for (int e = 0; e < 16; ++e)
-        if (e < from || e >= to) v[e] = 0xFF800000u;
-}
 
 template <int D>
 struct Smem {
@@ -277,11 +316,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
             if (!ok) break;
             tc::tc_fence_after();
             const ChunkScales* ts = scales[ms];
-            // does every row of the warp see all of the tile?
+            // does every row of the warp see all of the tile? If not, the scores that are not seen become
+            // -infinity in place, so that the two passes need not ask
             bool all = row_lo <= j0 && row_hi >= j0 + kTile;
             all &= ts[lane & (kChunks - 1)].ks >= 0.f;
-            const bool whole = __all_sync(0xffffffffu, all);
-            const int from = row_lo - j0, to = row_hi - j0;
+            if (!__all_sync(0xffffffffu, all)) {
+#pragma unroll 1
+                for (int c = 0; c < kChunks; ++c) {
+                    uint32_t v[16];
+                    tmem_ld_x16(s_at + 16u * c, v);
+                    tmem_ld_wait(v);
+                    const int from = ts[c].ks >= 0.f ? row_lo - j0 - 16 * c : 16, to = row_hi - j0 - 16 * c;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        if (e < from || e >= to) v[e] = 0xFF800000u;
+                    tc::tmem_st_x16_async(s_at + 16u * c, v);
+                }
+                tc::tmem_st_wait();
+            }
             // Scores are read twice, 32 at a time with the next 32 in flight, in rolled loops: the code of
             // the three roles has to stay in the instruction caches (unrolled, the warps waited for
             // instructions more than for anything else).
@@ -289,29 +341,31 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
             tmem_ld_x16(s_at, sv[0]);
             tmem_ld_x16(s_at + 16u, sv[1]);
             float mx = -INFINITY;
-            auto largest = [&](uint32_t (&v)[16], int c) {
-                const ChunkScales t = ts[c];
-                if (!whole) hide(v, t.ks >= 0.f ? from - 16 * c : 16, to - 16 * c);
-                float m[2] = {__uint_as_float(v[0]), __uint_as_float(v[1])};
+            auto largest = [&](const uint32_t (&v)[16]) {
+                float m0 = __uint_as_float(v[0]), m1 = __uint_as_float(v[1]);
 #pragma unroll
-                for (int e = 2; e < 16; ++e) m[e & 1] = fmaxf(m[e & 1], __uint_as_float(v[e]));
-                mx = fmaxf(mx, fmaf(fmaxf(m[0], m[1]), score_factor(zc, t.ks), t.lg));
+                for (int e = 2; e < 14; e += 4) {
+                    m0 = max3(m0, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+                    m1 = max3(m1, __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
+                }
+                return max3(fmaxf(m0, m1), __uint_as_float(v[14]), __uint_as_float(v[15]));
             };
 #pragma unroll 1
             for (int c = 0; c < kChunks; c += 4) {
+                ChunkScales t[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) t[x] = ts[c + x];
                 tmem_ld_wait(sv[0]);
                 tmem_ld_wait(sv[1]);
                 tmem_ld_x16(s_at + 16u * (c + 2), sv[2]);
                 tmem_ld_x16(s_at + 16u * (c + 3), sv[3]);
-                largest(sv[0], c);
-                largest(sv[1], c + 1);
+                mx = max3(mx, fmaf(largest(sv[0]), score_factor(zc, t[0].ks), t[0].lg), fmaf(largest(sv[1]), score_factor(zc, t[1].ks), t[1].lg));
                 tmem_ld_wait(sv[2]);
                 tmem_ld_wait(sv[3]);
                 const uint32_t next = s_at + 16u * ((c + 4) & (kChunks - 1));  // behind the last: the first again
                 tmem_ld_x16(next, sv[0]);
                 tmem_ld_x16(next + 16u, sv[1]);
-                largest(sv[2], c + 2);
-                largest(sv[3], c + 3);
+                mx = max3(mx, fmaf(largest(sv[2]), score_factor(zc, t[2].ks), t[2].lg), fmaf(largest(sv[3]), score_factor(zc, t[3].ks), t[3].lg));
             }
             const bool up = mx > ref + kSlack;
             if (__any_sync(0xffffffffu, up)) {
@@ -333,40 +387,52 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
                 }
             }
             const float minus_ref = kLift - (ref > -INFINITY ? ref : 0.f);
-            auto weigh = [&](uint32_t (&v)[16], int c) {  // chunk c's weights, as fp16 over scores that are done
-                const ChunkScales t = ts[c];
-                if (!whole) hide(v, t.ks >= 0.f ? from - 16 * c : 16, to - 16 * c);
-                const uint32_t k1 = __float_as_uint(score_factor(zc, t.ks)), b1 = __float_as_uint(t.lg + minus_ref);
-                const uint64_t k2 = tc::f2_pack(k1, k1), b2 = tc::f2_pack(b1, b1);
-                uint64_t sum = 0;
-                uint32_t pw[8];
+            // two chunks' weights, as fp16 over scores that are done
+            auto weigh = [&](const uint32_t (&va)[16], const uint32_t (&vb)[16], const ChunkScales& ta, const ChunkScales& tb, int c) {
+                uint32_t pw[16];
+                uint64_t sum[2][2] = {};
 #pragma unroll
-                for (int e = 0; e < 16; e += 2) {
-                    const uint64_t z = tc::f2_fma(tc::f2_pack(v[e], v[e + 1]), k2, b2);
-                    const float w0 = exp2_approx(__uint_as_float(static_cast<uint32_t>(z)));
-                    const float w1 = exp2_approx(__uint_as_float(static_cast<uint32_t>(z >> 32)));
-                    sum = f2_add(sum, tc::f2_pack(__float_as_uint(w0), __float_as_uint(w1)));
-                    pw[e / 2] = f2_to_h2(w0, w1);
+                for (int x = 0; x < 2; ++x) {
+                    const ChunkScales& t = x ? tb : ta;
+                    const uint32_t k1 = __float_as_uint(score_factor(zc, t.ks)), b1 = __float_as_uint(t.lg + minus_ref);
+                    const uint64_t k2 = tc::f2_pack(k1, k1), b2 = tc::f2_pack(b1, b1);
+#pragma unroll
+                    for (int e = 0; e < 16; e += 2) {
+                        const uint64_t z = tc::f2_fma(x ? tc::f2_pack(vb[e], vb[e + 1]) : tc::f2_pack(va[e], va[e + 1]), k2, b2);
+                        uint64_t w2;
+                        if (e == 2 || e == 8 || e == 14)  // three pairs of eight: both pipes take about as long
+                            w2 = f2_exp2(z);
+                        else
+                            w2 = tc::f2_pack(__float_as_uint(exp2_approx(__uint_as_float(static_cast<uint32_t>(z)))),
+                                             __float_as_uint(exp2_approx(__uint_as_float(static_cast<uint32_t>(z >> 32)))));
+                        sum[x][e / 2 & 1] = f2_add(sum[x][e / 2 & 1], w2);
+                        pw[8 * x + e / 2] = f2_to_h2(__uint_as_float(static_cast<uint32_t>(w2)), __uint_as_float(static_cast<uint32_t>(w2 >> 32)));
+                    }
                 }
-                l = fmaf(__uint_as_float(static_cast<uint32_t>(sum)) + __uint_as_float(static_cast<uint32_t>(sum >> 32)), t.inv, l);
-                tmem_st_x8_async(s_at + 8u * c, pw);
+                tmem_st_x16(s_at + 8u * c, pw);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const uint64_t all2 = f2_add(sum[x][0], sum[x][1]);
+                    l = fmaf(__uint_as_float(static_cast<uint32_t>(all2)) + __uint_as_float(static_cast<uint32_t>(all2 >> 32)), x ? tb.inv : ta.inv, l);
+                }
             };
 #pragma unroll 1
             for (int c = 0; c < kChunks; c += 4) {
+                ChunkScales t[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) t[x] = ts[c + x];
                 tmem_ld_wait(sv[0]);
                 tmem_ld_wait(sv[1]);
                 tmem_ld_x16(s_at + 16u * (c + 2), sv[2]);
                 tmem_ld_x16(s_at + 16u * (c + 3), sv[3]);
-                weigh(sv[0], c);
-                weigh(sv[1], c + 1);
+                weigh(sv[0], sv[1], t[0], t[1], c);
                 tmem_ld_wait(sv[2]);
                 tmem_ld_wait(sv[3]);
                 if (c + 4 < kChunks) {
                     tmem_ld_x16(s_at + 16u * (c + 4), sv[0]);
                     tmem_ld_x16(s_at + 16u * (c + 5), sv[1]);
                 }
-                weigh(sv[2], c + 2);
-                weigh(sv[3], c + 3);
+                weigh(sv[2], sv[3], t[2], t[3], c + 2);
             }
             tc::tmem_st_wait();
             tc::tc_fence_before();
@@ -379,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
         tc::tc_fence_after();
         if (ok) {
             const bool live = row < rows;
-            const float inv = bad ? NAN : l > 0.f || l != l ? vmax / l : 0.f;
+            const float inv = bad ? NAN : ref > -INFINITY ? vmax / l : 0.f;  // no reference: nothing was seen
             const int64_t at = p.splits > 1 ? out_row * p.splits + blockIdx.y : 0;
 #pragma unroll 2
             for (int c = 0; c < D / 16; ++c) {
@@ -411,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
                 }
             }
             if (live && p.splits > 1)
-                p.part_lse[at] = bad || l != l ? 0.f : l > 0.f ? ref - kLift + log2f(l) : -INFINITY;
+                p.part_lse[at] = bad ? 0.f : ref > -INFINITY ? ref - kLift + log2f(l) : -INFINITY;
         }
         tc::tc_fence_before();
     } else if (warp >= kConvertWarp0) {
@@ -510,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
             if (i < tiles && c == 0) mbar_arrive(&m_full[i & (kMeta - 1)]);
         }
       } else if (warp == kIssueWarp) {
-        if (lane == 0 && tiles > 0) {
+        if (tiles > 0) {
             // ------------------------------------------------------ the products
             constexpr uint32_t idesc_s = idesc_f16(128, kTile, 0), idesc_o = idesc_f16(128, D, 1);
             // everything but the tile's ring slot (kSub apart) is fixed
@@ -524,14 +590,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
                 for (int k = 0; k < D / 16; ++k) {
                     constexpr uint64_t kHalfUnits = L::kHalf >> 4;
                     const uint64_t off = (k >> 2) * kHalfUnits + (k & 3) * 2;
-                    tc::tc_mma(d, a + off, b + off, idesc_s, k > 0);
+                    mma_ss(d, a + off, b + off, idesc_s, k > 0);
                 }
             };
             auto pv = [&](int sub, int i) {
                 const uint64_t b = v_desc + (i & 1 ? 2 * kSubUnits : 0);
                 const uint32_t d = tmem + 256 + sub * D, a = tmem + sub * 128;
 #pragma unroll 2
-                for (int k = 0; k < kTile / 16; ++k) tc::tc_mma_ts(d, a + 8 * k, b + k * 128, idesc_o, i > 0 || k > 0);
+                for (int k = 0; k < kTile / 16; ++k) mma_ts(d, a + 8 * k, b + k * 128, idesc_o, i > 0 || k > 0);
             };
             ok = mbar_wait(&full[0], 0, 0x76);
             for (int sub = 0; ok && sub < 2; ++sub) {
@@ -539,9 +605,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
                 if (!ok) break;
                 tc::tc_fence_after();
                 qk(sub, 0);
-                tc::tc_commit(&s_full[sub]);
+                commit_elected(&s_full[sub]);
             }
-            if (ok) tc::tc_commit(&empty[0]);
+            if (ok) commit_elected(&empty[0]);
             for (int i = 0; ok && i < tiles; ++i) {
                 const uint32_t ph = (i >> 1) & 1, phn = ((i + 1) >> 1) & 1;
                 const int ks = 2 * ((i + 1) & 1), vs = 2 * (i & 1) + 1;
@@ -550,8 +616,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
                     if (!ok) break;
                     tc::tc_fence_after();
                     pv(sub, i);
-                    if (i + 1 == tiles) tc::tc_commit(&o_full[sub]);
-                    if (sub) tc::tc_commit(&empty[vs]);
+                    if (i + 1 == tiles) commit_elected(&o_full[sub]);
+                    if (sub) commit_elected(&empty[vs]);
                     if (i + 1 < tiles) {
                         if (!sub) {
                             ok = mbar_wait(&full[ks], phn, 0x7A);
@@ -559,8 +625,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
                             tc::tc_fence_after();
                         }
                         qk(sub, i + 1);
-                        tc::tc_commit(&s_full[sub]);
-                        if (sub) tc::tc_commit(&empty[ks]);
+                        commit_elected(&s_full[sub]);
+                        if (sub) commit_elected(&empty[ks]);
                     }
                 }
             }
