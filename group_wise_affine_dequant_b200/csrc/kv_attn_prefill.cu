@@ -40,8 +40,9 @@ constexpr int kIssueWarp = 0, kLookupWarp = 1, kSoftmaxWarp0 = 4, kSoftmaxWarps 
 constexpr int kThreads = 32 * 20;
 // Registers a thread by role: the block starts with kThreads * kRegsLaunch, and the
 // shares must not sum to more (a share that cannot be had would wait forever).
-constexpr int kRegsLaunch = 96, kRegsSoftmax = 136, kRegsConvert = 88, kRegsRest = 32;
+constexpr int kRegsLaunch = 96, kRegsSoftmax = 136, kRegsConvert = 80, kRegsRest = 48;
 static_assert(32 * kSoftmaxWarps * kRegsSoftmax + 32 * kConvertWarps * kRegsConvert + 128 * kRegsRest <= kThreads * kRegsLaunch, "");
+static_assert(kRegsConvert <= kRegsLaunch && kRegsRest <= kRegsLaunch && kRegsSoftmax >= kRegsLaunch, "dec lowers, inc raises");
 constexpr int kTmemCols = 512;
 constexpr int kMeta = 8;       // ring of per-tile lookups
 constexpr int kMetaBatch = 4;  // tiles looked up at once
@@ -81,11 +82,9 @@ __device__ __forceinline__ void tmem_ld_wait(uint32_t (&v)[16]) {
                  : "memory");
 }
 // No wait (tc::tmem_st_wait), and no claim on other memory: loads may move across.
-__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&v)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-        "%12, %13, %14, %15, %16};" ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]),
-        "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]));
+__device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t (&v)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]));
 }
 __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
     uint64_t d;
@@ -96,24 +95,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
-}
-// 2^z for two values on the FMA pipe (the special-function pipe, 16 results a clock and SM,
-// would be the limit with all of them): z = n + f, n the nearest integer (Cody and Waite's
-// reduction), 2^f on [-1/2, 1/2] by the cubic of least relative error (7.5e-5, 0.3 of an
-// fp16 rounding), n added to the exponent. z below -126 gives 2^-126, which fp16 rounds to 0.
-__device__ __forceinline__ uint64_t f2_exp2(uint64_t z) {
-    const float z0 = fmaxf(__uint_as_float(static_cast<uint32_t>(z)), -126.f);
-    const float z1 = fmaxf(__uint_as_float(static_cast<uint32_t>(z >> 32)), -126.f);
-    z = tc::f2_pack(__float_as_uint(z0), __float_as_uint(z1));
-    auto both = [](uint32_t c) { return tc::f2_pack(c, c); };
-    const uint64_t t = f2_add(z, both(0x4B400000u));                          // 1.5 * 2^23: n in the low bits
-    const uint64_t f = tc::f2_fma(f2_add(t, both(0xCB400000u)), both(0xBF800000u), z);
-    uint64_t p = tc::f2_fma(both(0x3D61FBB0u), f, both(0x3E786F0Du));         // 0.0551717, 0.242611
-    p = tc::f2_fma(p, f, both(0x3F31798Du));                                  // 0.693261
-    p = tc::f2_fma(p, f, both(0x3F7FFB49u));                                  // 0.999928
-    const uint32_t lo = static_cast<uint32_t>(p) + (static_cast<uint32_t>(t) << 23);
-    const uint32_t hi = static_cast<uint32_t>(p >> 32) + (static_cast<uint32_t>(t >> 32) << 23);
-    return tc::f2_pack(lo, hi);
 }
 // fp16 operands, fp32 accumulator; b_mn: B is read along N (MN-major).
 __host__ __device__ constexpr uint32_t idesc_f16(int m, int n, int b_mn) {
@@ -334,38 +315,30 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
                 }
                 tc::tmem_st_wait();
             }
-            // Scores are read twice, 32 at a time with the next 32 in flight, in rolled loops: the code of
+            // Scores are read twice, 16 at a time with the next 16 in flight, in rolled loops: the code of
             // the three roles has to stay in the instruction caches (unrolled, the warps waited for
             // instructions more than for anything else).
-            uint32_t sv[4][16];
+            uint32_t sv[2][16];
             tmem_ld_x16(s_at, sv[0]);
-            tmem_ld_x16(s_at + 16u, sv[1]);
             float mx = -INFINITY;
-            auto largest = [&](const uint32_t (&v)[16]) {
+            auto largest = [&](const uint32_t (&v)[16], const ChunkScales& t) {
                 float m0 = __uint_as_float(v[0]), m1 = __uint_as_float(v[1]);
 #pragma unroll
                 for (int e = 2; e < 14; e += 4) {
                     m0 = max3(m0, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
                     m1 = max3(m1, __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
                 }
-                return max3(fmaxf(m0, m1), __uint_as_float(v[14]), __uint_as_float(v[15]));
+                mx = fmaxf(mx, fmaf(max3(fmaxf(m0, m1), __uint_as_float(v[14]), __uint_as_float(v[15])), score_factor(zc, t.ks), t.lg));
             };
 #pragma unroll 1
-            for (int c = 0; c < kChunks; c += 4) {
-                ChunkScales t[4];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) t[x] = ts[c + x];
+            for (int c = 0; c < kChunks; c += 2) {
+                const ChunkScales ta = ts[c], tb = ts[c + 1];
                 tmem_ld_wait(sv[0]);
+                tmem_ld_x16(s_at + 16u * (c + 1), sv[1]);
+                largest(sv[0], ta);
                 tmem_ld_wait(sv[1]);
-                tmem_ld_x16(s_at + 16u * (c + 2), sv[2]);
-                tmem_ld_x16(s_at + 16u * (c + 3), sv[3]);
-                mx = max3(mx, fmaf(largest(sv[0]), score_factor(zc, t[0].ks), t[0].lg), fmaf(largest(sv[1]), score_factor(zc, t[1].ks), t[1].lg));
-                tmem_ld_wait(sv[2]);
-                tmem_ld_wait(sv[3]);
-                const uint32_t next = s_at + 16u * ((c + 4) & (kChunks - 1));  // behind the last: the first again
-                tmem_ld_x16(next, sv[0]);
-                tmem_ld_x16(next + 16u, sv[1]);
-                mx = max3(mx, fmaf(largest(sv[2]), score_factor(zc, t[2].ks), t[2].lg), fmaf(largest(sv[3]), score_factor(zc, t[3].ks), t[3].lg));
+                tmem_ld_x16(s_at + 16u * ((c + 2) & (kChunks - 1)), sv[0]);  // behind the last: the first again
+                largest(sv[1], tb);
             }
             const bool up = mx > ref + kSlack;
             if (__any_sync(0xffffffffu, up)) {
@@ -387,53 +360,38 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
                 }
             }
             const float minus_ref = kLift - (ref > -INFINITY ? ref : 0.f);
-            // two chunks' weights, as fp16 over scores that are done
-            auto weigh = [&](const uint32_t (&va)[16], const uint32_t (&vb)[16], const ChunkScales& ta, const ChunkScales& tb, int c) {
-                uint32_t pw[16];
-                uint64_t sum[2][2] = {};
+            // a chunk's weights, as fp16 over scores that are done
+            auto weigh = [&](const uint32_t (&v)[16], const ChunkScales& t, int c) {
+                uint32_t pw[8];
+                uint64_t sum[2] = {};
+                const uint32_t k1 = __float_as_uint(score_factor(zc, t.ks)), b1 = __float_as_uint(t.lg + minus_ref);
+                const uint64_t k2 = tc::f2_pack(k1, k1), b2 = tc::f2_pack(b1, b1);
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const ChunkScales& t = x ? tb : ta;
-                    const uint32_t k1 = __float_as_uint(score_factor(zc, t.ks)), b1 = __float_as_uint(t.lg + minus_ref);
-                    const uint64_t k2 = tc::f2_pack(k1, k1), b2 = tc::f2_pack(b1, b1);
-#pragma unroll
-                    for (int e = 0; e < 16; e += 2) {
-                        const uint64_t z = tc::f2_fma(x ? tc::f2_pack(vb[e], vb[e + 1]) : tc::f2_pack(va[e], va[e + 1]), k2, b2);
-                        uint64_t w2;
-                        if (e == 2 || e == 8 || e == 14)  // three pairs of eight: both pipes take about as long
-                            w2 = f2_exp2(z);
-                        else
-                            w2 = tc::f2_pack(__float_as_uint(exp2_approx(__uint_as_float(static_cast<uint32_t>(z)))),
-                                             __float_as_uint(exp2_approx(__uint_as_float(static_cast<uint32_t>(z >> 32)))));
-                        sum[x][e / 2 & 1] = f2_add(sum[x][e / 2 & 1], w2);
-                        pw[8 * x + e / 2] = f2_to_h2(__uint_as_float(static_cast<uint32_t>(w2)), __uint_as_float(static_cast<uint32_t>(w2 >> 32)));
-                    }
+                for (int e = 0; e < 16; e += 2) {
+                    const uint64_t z = tc::f2_fma(tc::f2_pack(v[e], v[e + 1]), k2, b2);
+                    const float w0 = exp2_approx(__uint_as_float(static_cast<uint32_t>(z)));
+                    const float w1 = exp2_approx(__uint_as_float(static_cast<uint32_t>(z >> 32)));
+                    sum[e / 2 & 1] = f2_add(sum[e / 2 & 1], tc::f2_pack(__float_as_uint(w0), __float_as_uint(w1)));
+                    pw[e / 2] = f2_to_h2(w0, w1);
                 }
-                tmem_st_x16(s_at + 8u * c, pw);
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const uint64_t all2 = f2_add(sum[x][0], sum[x][1]);
-                    l = fmaf(__uint_as_float(static_cast<uint32_t>(all2)) + __uint_as_float(static_cast<uint32_t>(all2 >> 32)), x ? tb.inv : ta.inv, l);
-                }
+                tmem_st_x8(s_at + 8u * c, pw);
+                sum[0] = f2_add(sum[0], sum[1]);
+                l = fmaf(__uint_as_float(static_cast<uint32_t>(sum[0])) + __uint_as_float(static_cast<uint32_t>(sum[0] >> 32)), t.inv, l);
             };
+            ChunkScales ta = ts[0], tb = ts[1];
 #pragma unroll 1
-            for (int c = 0; c < kChunks; c += 4) {
-                ChunkScales t[4];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) t[x] = ts[c + x];
+            for (int c = 0; c < kChunks; c += 2) {
+                const int next = (c + 2) & (kChunks - 1);
                 tmem_ld_wait(sv[0]);
+                tmem_ld_x16(s_at + 16u * (c + 1), sv[1]);
+                weigh(sv[0], ta, c);
+                ta = ts[next];
                 tmem_ld_wait(sv[1]);
-                tmem_ld_x16(s_at + 16u * (c + 2), sv[2]);
-                tmem_ld_x16(s_at + 16u * (c + 3), sv[3]);
-                weigh(sv[0], sv[1], t[0], t[1], c);
-                tmem_ld_wait(sv[2]);
-                tmem_ld_wait(sv[3]);
-                if (c + 4 < kChunks) {
-                    tmem_ld_x16(s_at + 16u * (c + 4), sv[0]);
-                    tmem_ld_x16(s_at + 16u * (c + 5), sv[1]);
-                }
-                weigh(sv[2], sv[3], t[2], t[3], c + 2);
+                tmem_ld_x16(s_at + 16u * next, sv[0]);  // behind the last: nobody's
+                weigh(sv[1], tb, c + 1);
+                tb = ts[next + 1];
             }
+            tmem_ld_wait(sv[0]);
             tc::tmem_st_wait();
             tc::tc_fence_before();
             mbar_arrive(&p_full[sub]);
@@ -688,6 +646,8 @@ cudaError_t launch(const PrefillArgs& p, cudaStream_t stream) {
         return cudaFuncGetAttributes(&at, kv_attn_prefill_kernel<MODE, D>) == cudaSuccess ? at.numRegs : 0;
     }();
     if (regs < kRegsLaunch) return cudaErrorLaunchOutOfResources;
+    // Not launched programmatically: its CTAs take a whole SM each, and early ones only keep the last
+    // of the kernel before it from theirs (ragged chunks, behind the kernel for few rows: 335 -> 320 us).
     cudaLaunchAttribute pdl[1];
     pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     pdl[0].val.programmaticStreamSerializationAllowed = 1;
@@ -696,10 +656,10 @@ cudaError_t launch(const PrefillArgs& p, cudaStream_t stream) {
     cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.dynamicSmemBytes = Smem<D>::kBytes;
     cfg.stream = stream;
-    cfg.attrs = pdl;
-    cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, kv_attn_prefill_kernel<MODE, D>, p);
     if (e != cudaSuccess || p.splits <= 1) return e;
+    cfg.attrs = pdl;
+    cfg.numAttrs = 1;
     cfg.gridDim = dim3(static_cast<unsigned>((p.st.rows * p.a.Hq + 3) / 4), 1, 1);
     cfg.blockDim = dim3(128, 1, 1);
     cfg.dynamicSmemBytes = 0;
