@@ -9,6 +9,7 @@ library is missing or a call fails, an exception says so.
 from __future__ import annotations
 
 import ctypes as C
+import importlib.util
 import os
 import threading
 
@@ -39,7 +40,6 @@ _FP_GROUP = {"mxfp4": 32, "mxfp8": 32, "nvfp4": 16}
 _FP_BITS = {"mxfp4": 4, "mxfp8": 8, "nvfp4": 4}
 
 NV_KV_INT8, NV_KV_E4M3 = 1, 2
-_KV_MODES = {torch.int8: NV_KV_INT8, torch.float8_e4m3fn: NV_KV_E4M3}
 _ROUTE_SCORES = {"softmax": 0, "sigmoid": 1}
 
 _DT = {torch.float32: NV_F32, torch.bfloat16: NV_BF16}
@@ -481,19 +481,26 @@ def nv_qmm_fp(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, mode: 
     return y
 
 
-# The current stream's handle without building a Stream object around it (4 us a call
-# where the calls below take 10 in all).
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
-    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_CALLS = None
 
 
-def _call(fn, index: int, stream, *args) -> int:
-    """fn(*args, stream) on device `index`, made current for the call where it is
-    not; stream None is that device's current stream."""
-    if index != torch.cuda.current_device():
-        with torch.cuda.device(index):
-            return fn(*args, _raw_stream(index) if stream is None else _stream(stream))
-    return fn(*args, _raw_stream(index) if stream is None else _stream(stream))
+def _calls():
+    """The extension module that marshals the calls below (csrc/torch_calls.cpp), bound to
+    the loaded library; built first if it is missing. It raises ValueError for tensors
+    that do not fit and returns the outputs, or the status of a refused call."""
+    global _CALLS
+    if _CALLS is None:
+        L = lib()
+        if not os.path.exists(_build.CALLS):
+            _build.build_calls()
+        spec = importlib.util.spec_from_file_location("_calls", _build.CALLS)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.bind(*(C.cast(f, C.c_void_p).value for f in (
+            L.nv_moe_route, L.nv_kv_quantize, L.nv_kv_dequantize, L.nv_kv_attention,
+            L.nv_kv_attention_workspace_size)))
+        _CALLS = module
+    return _CALLS
 
 
 def nv_moe_route(logits: torch.Tensor, topk: int, score: str = "softmax",
@@ -504,70 +511,14 @@ def nv_moe_route(logits: torch.Tensor, topk: int, score: str = "softmax",
     nv_moe_swiglu takes as ids and rw. score 'softmax' or 'sigmoid'; bias fp32 [E]
     is added for the choice only; with groups > 1 only the topk_groups best groups
     are chosen from (a group's score: its group_top = 1 or 2 largest, summed)."""
-    _dev(logits, "logits")
-    if logits.dim() != 2 or score not in _ROUTE_SCORES:
-        raise ValueError(f"logits must be [T, E] and score one of {sorted(_ROUTE_SCORES)}")
-    T, E = logits.shape
-    device, index = logits.device, logits.get_device()
-    if bias is not None and (bias.get_device() != index or bias.dtype != torch.float32 or
-                             bias.numel() != E or not bias.is_contiguous()):
-        raise ValueError("bias must be contiguous fp32 [E] on the logits' device")
-    if ids is None:
-        ids = torch.empty((T, max(topk, 0)), dtype=torch.int32, device=device)
-    elif tuple(ids.shape) != (T, topk) or ids.dtype != torch.int32 or ids.get_device() != index or \
-            not ids.is_contiguous():
-        raise ValueError("ids must be contiguous int32 [T, topk] on the logits' device")
-    if weights is None:
-        weights = torch.empty((T, max(topk, 0)), dtype=torch.float32, device=device)
-    elif tuple(weights.shape) != (T, topk) or weights.dtype != torch.float32 or \
-            weights.get_device() != index or not weights.is_contiguous():
-        raise ValueError("weights must be contiguous fp32 [T, topk] on the logits' device")
-    st = _call(lib().nv_moe_route, index, stream, logits.data_ptr(), _DT.get(logits.dtype, -1), T, E,
-               None if bias is None else bias.data_ptr(), _ROUTE_SCORES[score], groups,
-               groups if topk_groups is None else topk_groups, group_top, topk, int(renormalize), scale,
-               ids.data_ptr(), weights.data_ptr())
-    _check("nv_moe_route", st)
-    return ids, weights
-
-
-def _kv_args(k_codes, k_scales, v_codes, v_scales, pages, starts, lens, flags):
-    """The cache's and the step descriptor's arguments as the C calls take them,
-    after the checks that need shapes: (cache, steps, flags pointer, device index)."""
-    index = k_codes.get_device()
-    for t in (k_codes, k_scales, v_codes, v_scales, pages, starts, lens):
-        if t.get_device() != index or not t.is_contiguous():
-            index = -1
-    if index < 0:
-        raise ValueError("the cache, pages, starts and lens must be contiguous CUDA tensors on one device")
-    shape, dtype = k_codes.shape, k_codes.dtype
-    mode = _KV_MODES.get(dtype)
-    if len(shape) != 4 or shape != v_codes.shape or dtype != v_codes.dtype or mode is None:
-        raise ValueError("k_codes and v_codes must be int8 or float8_e4m3fn [P, H, block, D] alike")
-    if k_scales.shape != shape[:2] or v_scales.shape != shape[:2] or \
-            not (k_scales.dtype == v_scales.dtype == torch.float32):
-        raise ValueError("k_scales and v_scales must be fp32 [P, H]")
-    table = pages.shape
-    S = table[0]
-    if len(table) != 2 or starts.shape != (S + 1,) or lens.shape != (S,):
-        raise ValueError("pages [S, max_pages], starts [S + 1] and lens [S] expected")
-    if not (pages.dtype == starts.dtype == lens.dtype == torch.int32):
-        raise ValueError("pages, starts and lens must be int32")
-    if flags is not None:
-        if flags.get_device() != index or flags.dtype != torch.int32 or flags.numel() < 1:
-            raise ValueError("flags must be an int32 CUDA tensor on the cache's device")
-        flags = flags.data_ptr()
-    return ((k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), mode, *shape),
-            (pages.data_ptr(), table[1], starts.data_ptr(), lens.data_ptr(), S), flags, index)
-
-
-def _kv_rows(t: torch.Tensor, name: str, heads: int, D: int, index: int) -> int:
-    """Row stride of a step's tensor [rows, heads, D]: dense heads, any distance between rows."""
-    if t.get_device() != index or t.dim() != 3 or t.shape[1:] != (heads, D):
-        raise ValueError(f"{name} must be [rows, {heads}, {D}] on the cache's device")
-    row, head, last = t.stride()
-    if (last != 1 and D > 1) or (head != D and heads > 1):
-        raise ValueError(f"the heads of a row of {name} must be dense")
-    return row if t.shape[0] > 1 else heads * D
+    if score not in _ROUTE_SCORES:
+        raise ValueError(f"score must be one of {sorted(_ROUTE_SCORES)}")
+    r = (_CALLS or _calls()).moe_route(
+        logits, topk, _ROUTE_SCORES[score], bias, groups, groups if topk_groups is None else topk_groups, group_top,
+        renormalize, scale, ids, weights, None if stream is None else _stream(stream))
+    if type(r) is int:
+        _check("nv_moe_route", r)
+    return r
 
 
 def nv_kv_quantize(k: torch.Tensor, v: torch.Tensor, k_codes: torch.Tensor, k_scales: torch.Tensor,
@@ -578,14 +529,9 @@ def nv_kv_quantize(k: torch.Tensor, v: torch.Tensor, k_codes: torch.Tensor, k_sc
     paged 8-bit cache: codes int8 or float8_e4m3fn [P, H, block, D], scales fp32
     [P, H]. Rows starts[s] .. starts[s + 1] are the last tokens of sequence s,
     lens[s] its length with them, pages[s, j] the page of its j-th block."""
-    cache, steps, fl, index = _kv_args(k_codes, k_scales, v_codes, v_scales, pages, starts, lens, flags)
-    H, D = cache[6], cache[8]
-    ks, vs = _kv_rows(k, "k", H, D, index), _kv_rows(v, "v", H, D, index)
-    if k.shape != v.shape or k.dtype != v.dtype:
-        raise ValueError("k and v must be alike")
-    st = _call(lib().nv_kv_quantize, index, stream, k.data_ptr(), v.data_ptr(), ks, vs,
-               _DT.get(k.dtype, -1), k.shape[0], *cache, *steps, fl)
-    _check("nv_kv_quantize", st)
+    _check("nv_kv_quantize", (_CALLS or _calls()).kv_quantize(
+        k, v, k_codes, k_scales, v_codes, v_scales, pages, starts, lens, flags,
+        None if stream is None else _stream(stream)))
 
 
 def nv_kv_dequantize(k_codes: torch.Tensor, k_scales: torch.Tensor, v_codes: torch.Tensor,
@@ -595,20 +541,13 @@ def nv_kv_dequantize(k_codes: torch.Tensor, k_scales: torch.Tensor, v_codes: tor
     """(k, v) [rows, H, D]: the last starts[s + 1] - starts[s] tokens of every
     sequence, read back (all of them where starts is the running sum of lens).
     out: a pair of tensors to write to; rows of no sequence are left as they were."""
-    cache, steps, fl, index = _kv_args(k_codes, k_scales, v_codes, v_scales, pages, starts, lens, flags)
-    shape = (rows, cache[6], cache[8])
-    if out is None:
-        device = k_codes.device
-        k, v = torch.empty(shape, dtype=dtype, device=device), torch.empty(shape, dtype=dtype, device=device)
-    else:
-        k, v = out
-        for t in out:
-            if t.shape != shape or t.dtype != dtype or t.get_device() != index or not t.is_contiguous():
-                raise ValueError(f"out must be two contiguous {dtype} {shape} tensors on the cache's device")
-    st = _call(lib().nv_kv_dequantize, index, stream, *cache, *steps, _DT.get(dtype, -1), rows,
-               k.data_ptr(), v.data_ptr(), fl)
-    _check("nv_kv_dequantize", st)
-    return k, v
+    k, v = (None, None) if out is None else out
+    r = (_CALLS or _calls()).kv_dequantize(
+        k_codes, k_scales, v_codes, v_scales, pages, starts, lens, flags, rows, dtype, k, v,
+        None if stream is None else _stream(stream))
+    if type(r) is int:
+        _check("nv_kv_dequantize", r)
+    return r
 
 
 def nv_kv_attention_workspace_size(rows: int, Hq: int, H: int, block: int, D: int, max_pages: int, S: int,
@@ -628,29 +567,9 @@ def nv_kv_attention(q: torch.Tensor, k_codes: torch.Tensor, k_scales: torch.Tens
     defaults to D ** -0.5; window > 0 limits a causal row to its last `window`
     tokens; max_q is the largest number of rows of one sequence, if known.
     Returns out [rows, Hq, D]; rows of no sequence are left as they were."""
-    cache, steps, fl, index = _kv_args(k_codes, k_scales, v_codes, v_scales, pages, starts, lens, flags)
-    if index != torch.cuda.current_device():  # the workspace's size goes by that device too
-        with torch.cuda.device(index):
-            return nv_kv_attention(q, k_codes, k_scales, v_codes, v_scales, pages, starts, lens, scale, causal,
-                                   window, max_q, workspace, out, flags, stream)
-    H, block, D = cache[6:]
-    if q.dim() != 3:
-        raise ValueError("q must be [rows, Hq, D]")
-    rows, Hq = q.shape[:2]
-    qs = _kv_rows(q, "q", Hq, D, index)
-    if out is None:
-        out = torch.empty((rows, Hq, D), dtype=q.dtype, device=q.device)
-    elif out.shape != q.shape or out.dtype != q.dtype or out.get_device() != index or not out.is_contiguous():
-        raise ValueError("out must be contiguous and like q")
-    L, dt = lib(), _DT.get(q.dtype, -1)
-    if workspace is None:
-        need = L.nv_kv_attention_workspace_size(dt, rows, Hq, H, block, D, steps[1], steps[4], max_q)
-        if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    elif workspace.get_device() != index or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous CUDA tensor on the cache's device")
-    wp, wb = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
-    st = _call(L.nv_kv_attention, index, stream, q.data_ptr(), qs, dt, rows, Hq, *cache, *steps,
-               D ** -0.5 if scale is None else scale, int(causal), window, max_q, wp, wb, out.data_ptr(), fl)
-    _check("nv_kv_attention", st)
-    return out
+    r = (_CALLS or _calls()).kv_attention(
+        q, k_codes, k_scales, v_codes, v_scales, pages, starts, lens, flags, scale, causal, window, max_q, workspace,
+        out, None if stream is None else _stream(stream))
+    if type(r) is int:
+        _check("nv_kv_attention", r)
+    return r

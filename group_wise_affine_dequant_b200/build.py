@@ -1,18 +1,23 @@
-"""Build libnvq.so, the C-ABI library, in-tree for sm_100a.
+"""Build libnvq.so, the C-ABI library, in-tree for sm_100a, and the Python
+extension module _calls that marshals torch tensors into its serving calls.
 
     python -m group_wise_affine_dequant_b200.build
 
 Each .cu file under csrc/ compiles to an object in _build/ (in parallel), then
 nvcc links them into group_wise_affine_dequant_b200/libnvq.so. The CUDA runtime
 is linked statically, so the library needs only the NVIDIA driver at run time.
+The extension (csrc/torch_calls.cpp, g++ against the installed torch's headers and
+Python's) holds no kernels and does not link libnvq.so.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
 import os
+import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -32,11 +37,36 @@ def _headers():
     return sorted(glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
+CALLS_SRC = os.path.join(CSRC, "torch_calls.cpp")
+CALLS = os.path.join(HERE, "_calls.so")
+
+
+def build_calls() -> str:
+    """Compile the extension module _calls."""
+    import torch
+
+    home = os.path.dirname(torch.__file__)
+    nvcc = shutil.which(NVCC)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc))) if nvcc else "/usr/local/cuda"
+    tmp = CALLS + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++20", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f"-I{home}/include",
+           f"-I{home}/include/torch/csrc/api/include", "-I" + sysconfig.get_paths()["include"], f"-I{cuda}/include",
+           CALLS_SRC, "-o", tmp, f"-L{home}/lib", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda",
+           "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed on {CALLS_SRC}:\n{r.stderr}")
+    os.replace(tmp, CALLS)
+    return CALLS
+
+
 def stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(CALLS):
         return True
     t = os.path.getmtime(LIB)
-    return any(os.path.getmtime(f) > t for f in _sources() + _headers())
+    return any(os.path.getmtime(f) > t for f in _sources() + _headers()) or \
+        os.path.getmtime(CALLS_SRC) > os.path.getmtime(CALLS)
 
 
 def _compile(src: str, verbose: bool) -> str:
@@ -55,8 +85,10 @@ def _compile(src: str, verbose: bool) -> str:
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = _sources()
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs)) + 1) as ex:
+        calls = ex.submit(build_calls)
         objs = list(ex.map(lambda s: _compile(s, verbose), srcs))
+        calls.result()
     tmp = LIB + ".tmp"
     cmd = [NVCC, *ARCH, "-shared", "-o", tmp, *objs]
     subprocess.run(cmd, check=True)
