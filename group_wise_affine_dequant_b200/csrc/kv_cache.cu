@@ -69,27 +69,23 @@ struct Raw8<NV_F32> {
     }
 };
 
-// The integer nearest to x / s (ties to even), |x / s| <= 127.5: a first guess
-// by the reciprocal is off by at most one, and the remainder x - c s is exact
-// in fp32 (both are multiples of s's unit, below 2 s), so comparing it with
-// s / 2 settles the guess. Returned as magic + c, whose low byte is the code.
+// int8: the integer nearest to x / s (ties to even), |x / s| <= 127.5. A first guess
+// c by the reciprocal is off by at most one, and the remainder x - c s is exact in
+// fp32 (both are multiples of s's unit, below 2 s): the guess stands where it is below s / 2.
+// kMagic + c holds c in its low byte.
 constexpr float kMagic = 12582912.f;  // 1.5 * 2^23
-__device__ __forceinline__ uint32_t int8_code(float x, float s, float inv) {
+__device__ __forceinline__ uint32_t int8_exact(float x, float s, float inv) {
     float t = fmaf(x, inv, kMagic);
-    const float c = t - kMagic;
-    const float e = fmaf(-c, s, x), half = 0.5f * s;
-    if (fabsf(e) >= half) {
-        const bool odd = __float_as_uint(t) & 1u;
-        if (fabsf(e) > half || odd) t += copysignf(1.f, e);
-    }
-    t = fminf(fmaxf(t, kMagic - kInt8Max), kMagic + kInt8Max);
-    return __float_as_uint(t) & 0xFFu;
+    const float e = fmaf(-(t - kMagic), s, x), half = 0.5f * s;
+    const bool odd = __float_as_uint(t) & 1u;
+    if (fabsf(e) > half || (fabsf(e) == half && odd)) t += copysignf(1.f, e);
+    return __float_as_uint(t);
 }
 
-// x / s as a float that rounds to E4M3 as the exact quotient does: only a
-// quotient that landed on a 5-bit value (a tie's place) by rounding is moved
-// off it, by one unit towards the exact value.
-__device__ __forceinline__ float e4m3_quotient(float x, float s) {
+// E4M3: x / s as a float that rounds as the exact quotient does: only a quotient
+// that landed on a 5-bit value (a tie's place) by rounding is moved off it, by one
+// unit towards the exact value.
+__device__ __forceinline__ float e4m3_exact(float x, float s) {
     const float q = __fdiv_rn(x, s);
     if ((__float_as_uint(q) & 0x3FFFFu) == 0u) {
         const float r = fmaf(-q, s, x);
@@ -99,22 +95,47 @@ __device__ __forceinline__ float e4m3_quotient(float x, float s) {
     return q;
 }
 
+// Eight codes. The quick form settles all but what lies next to a tie, which is rare
+// enough to be asked once for the eight: an E4M3 quotient by the reciprocal (two
+// units off at most) rounds as the exact one unless its low 20 bits are within 4 of a
+// half, or it is small enough for E4M3's subnormals.
 template <int MODE>
 __device__ __forceinline__ uint2 encode8(const float (&x)[8], float s, float inv) {
     uint32_t w[2];
+    if constexpr (MODE == NV_KV_INT8) {
+        uint32_t t[8];
+        bool near = false;
+        const float half = 0.5f * s;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        if constexpr (MODE == NV_KV_INT8) {
-            uint32_t b[4];
+        for (int j = 0; j < 8; ++j) {
+            const float m = fmaf(x[j], inv, kMagic);
+            near |= fabsf(fmaf(-(m - kMagic), s, x[j])) >= half;
+            t[j] = __float_as_uint(m);
+        }
+        if (near) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) b[j] = int8_code(x[4 * h + j], s, inv);
-            w[h] = b[0] | (b[1] << 8) | (b[2] << 16) | (b[3] << 24);
-        } else {
-            float q[4];
+            for (int j = 0; j < 8; ++j) t[j] = int8_exact(x[j], s, inv);
+        }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) q[j] = e4m3_quotient(x[4 * h + j], s);
-            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(q[0], q[1]), __NV_SATFINITE, __NV_E4M3);
-            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(q[2], q[3]), __NV_SATFINITE, __NV_E4M3);
+        for (int h = 0; h < 2; ++h)
+            w[h] = __byte_perm(__byte_perm(t[4 * h], t[4 * h + 1], 0x0040), __byte_perm(t[4 * h + 2], t[4 * h + 3], 0x0040), 0x5410);
+    } else {
+        float q[8];
+        bool near = false;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            q[j] = x[j] * inv;
+            const uint32_t u = __float_as_uint(q[j]);
+            near |= (u - 0x7FFFCu & 0xFFFFFu) <= 8u || (u & 0x7FFFFFFFu) - 1u < 0x3C800000u - 1u;  // 2^-6, zero is exact
+        }
+        if (near) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) q[j] = e4m3_exact(x[j], s);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(q[4 * h], q[4 * h + 1]), __NV_SATFINITE, __NV_E4M3);
+            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(q[4 * h + 2], q[4 * h + 3]), __NV_SATFINITE, __NV_E4M3);
             w[h] = lo | (hi << 16);
         }
     }
@@ -139,7 +160,7 @@ __device__ __forceinline__ uint8_t recode(uint32_t byte, float old_scale, float 
 
 // The block of tokens a CTA works on: sequence, page and this step's slots in it.
 struct BlockWork {
-    int page;          // -1: out of range (flagged) or nothing to do
+    int page;          // the table's entry, not yet looked at (page_ok); -1: nothing to do
     int slot0, slot1;  // the step's tokens in the block
     int64_t row0;      // row of slot0
     bool any;          // the block has tokens of the step
@@ -156,14 +177,29 @@ __device__ __forceinline__ BlockWork block_work(const KvCache& c, const KvSteps&
     w.slot0 = first > base ? first - base : 0;
     w.slot1 = span.len - base < c.block ? span.len - base : c.block;
     w.row0 = span.row0 + (base + w.slot0 - span.first);
-    w.page = page_of(st, c, s, static_cast<int>(b));
+    w.page = __ldg(st.pages + static_cast<int64_t>(s) * st.max_pages + b);
     return w;
 }
+// Kept apart from the lookup, so that a block's values are on their way before its page is known.
+__device__ __forceinline__ bool page_ok(const KvCache& c, const KvSteps& st, const BlockWork& w) {
+    if (w.page >= 0 && w.page < c.P) return true;
+    if (st.flags) atomicOr(st.flags, NV_FLAG_PAGE_OUT_OF_RANGE);
+    return false;
+}
+
+// i / d for 0 <= i < 2^16, by one multiplication: magic = 2^32 / d rounded up, which is
+// exact there since i times its error (below d / 2^32 a unit) stays under 1 / d.
+struct Divider {
+    uint32_t d, magic;
+    explicit Divider(uint32_t n) : d(n), magic(n == 1 ? 0u : static_cast<uint32_t>(((1ull << 32) + n - 1) / n)) {}
+    __device__ __forceinline__ int of(int i) const { return d == 1 ? i : static_cast<int>(__umulhi(i, magic)); }
+};
 
 struct QuantArgs {
     const void* x[2];  // k, v
     int64_t stride[2];
     int planes;        // planes a CTA takes
+    Divider vecs;      // 8-value chunks a token
     KvCache c;
     KvSteps st;
 };
@@ -179,12 +215,9 @@ __device__ __forceinline__ void quantize_plane(const QuantArgs& a, const BlockWo
     const int chunks = (w.slot1 - w.slot0) * vecs;
     const void* x = which ? a.x[1] : a.x[0];
     const int64_t stride = which ? a.stride[1] : a.stride[0];
-    const int64_t at = static_cast<int64_t>(w.page) * c.H + h;
-    uint8_t* codes = (which ? c.v_codes : c.k_codes) + at * (static_cast<int64_t>(c.block) * c.D);
-    float* scale_at = (which ? c.v_scales : c.k_scales) + at;
     const int64_t x0 = w.row0 * stride + static_cast<int64_t>(h) * c.D;
     auto place = [&](int i) {  // chunk i's first value
-        const int tok = i / vecs;
+        const int tok = a.vecs.of(i);
         return x0 + tok * stride + (i - tok * vecs) * 8;
     };
     Raw8<DT> keep[kKeep];
@@ -193,6 +226,10 @@ __device__ __forceinline__ void quantize_plane(const QuantArgs& a, const BlockWo
         keep[k].clear();
         if (rank + k * size < chunks) keep[k].load(x, place(rank + k * size));
     }
+    if (!page_ok(c, a.st, w)) return;  // the same for the whole team
+    const int64_t at = static_cast<int64_t>(w.page) * c.H + h;
+    uint8_t* codes = (which ? c.v_codes : c.k_codes) + at * (static_cast<int64_t>(c.block) * c.D);
+    float* scale_at = (which ? c.v_scales : c.k_scales) + at;
     const float old = w.slot0 > 0 ? *scale_at : 0.f;
     uint32_t most = 0;
 #pragma unroll
@@ -283,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 3) kv_quantize_kernel(const __grid_c
     const int s = kv_find_seq(a.st, blockIdx.x, 1, a.c.block, 2);
     const SeqSpan span = seq_span(a.st, s, a.c.block);
     const BlockWork w = block_work(a.c, a.st, span, s, static_cast<int64_t>(blockIdx.x) - kv_first_item(a.st, s, 1, a.c.block, 2));
-    if (w.page < 0) return;
+    if (!w.any) return;
     const int p0 = blockIdx.y * a.planes;
     const int p1 = p0 + a.planes < 2 * a.c.H ? p0 + a.planes : 2 * a.c.H;
     if ((w.slot1 - w.slot0) * (a.c.D / 8) <= 32 * kKeep) {
@@ -309,9 +346,29 @@ __global__ void __launch_bounds__(kThreads, 3) kv_quantize_kernel(const __grid_c
     }
 }
 
+// Four codes as floats (exact).
+template <int MODE>
+__device__ __forceinline__ void word_values(uint32_t w, float* f) {
+    if constexpr (MODE == NV_KV_INT8) {
+        w ^= 0x80808080u;  // c + 128
+#pragma unroll
+        for (int i = 0; i < 4; ++i)  // under the mantissa of 2^23
+            f[i] = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440 | i)) - 8388736.f;
+    } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const __half2_raw v = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> (16 * h)), __NV_E4M3);
+            const float2 x = __half22float2(__half2(v));
+            f[2 * h] = x.x;
+            f[2 * h + 1] = x.y;
+        }
+    }
+}
+
 struct DequantArgs {
     void* out[2];  // k, v [rows, H, D]
     int planes;
+    Divider vecs;  // 16-value chunks a token
     KvCache c;
     KvSteps st;
 };
@@ -355,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 4) kv_dequantize_kernel(const __grid
     }
     if (!w.any) return;
     const int chunks = (w.slot1 - w.slot0) * vecs;
-    if (w.page < 0) {
+    if (!page_ok(c, a.st, w)) {
         for (int i = threadIdx.x; i < chunks * count; i += kThreads) {
             const int p = i / chunks, k = i - p * chunks, tok = k / vecs;
             store(p0 + p, w.row0 + tok, (k - tok * vecs) * 16, zeros);
@@ -364,29 +421,41 @@ __global__ void __launch_bounds__(kThreads, 4) kv_dequantize_kernel(const __grid
     }
     const int64_t bytes = static_cast<int64_t>(c.block) * c.D;
     constexpr int kUnroll = 4;
-    for (int i0 = threadIdx.x; i0 < chunks * count; i0 += kThreads * kUnroll) {
-        uint4 u[kUnroll];
-        float scale[kUnroll];
+    // thread = (plane of the run, chunk): chunks * count stays below 2^16 but for runs of many heads of
+    // large blocks, which take the planes in several rounds
+    const int fit = 0xFFFF / chunks < count ? 0xFFFF / chunks : count;
+    const float by_chunk = 1.f / static_cast<float>(chunks);
+    for (int first = 0; first < count; first += fit) {
+        const int planes = count - first < fit ? count - first : fit;
+        for (int i0 = threadIdx.x; i0 < chunks * planes; i0 += kThreads * kUnroll) {
+            uint4 u[kUnroll];
+            float scale[kUnroll];
+            int plane[kUnroll], k[kUnroll];
 #pragma unroll
-        for (int n = 0; n < kUnroll; ++n) {
-            const int i = i0 + n * kThreads;
-            if (i >= chunks * count) break;
-            const int p = i / chunks, k = i - p * chunks, plane = p0 + p;
-            const int64_t at = static_cast<int64_t>(w.page) * c.H + (plane >> 1);
-            u[n] = __ldg(reinterpret_cast<const uint4*>((plane & 1 ? c.v_codes : c.k_codes) + at * bytes +
-                                                       static_cast<int64_t>(w.slot0) * c.D + 16 * static_cast<int64_t>(k)));
-            scale[n] = __ldg((plane & 1 ? c.v_scales : c.k_scales) + at);
-        }
+            for (int n = 0; n < kUnroll; ++n) {
+                const int i = i0 + n * kThreads;
+                if (i >= chunks * planes) break;
+                // i / chunks: the quotient of two integers below 2^16, rounded down, from its fp32 value
+                int q = static_cast<int>((static_cast<float>(i) + 0.5f) * by_chunk);
+                plane[n] = p0 + first + q;
+                k[n] = i - q * chunks;
+                const int64_t at = static_cast<int64_t>(w.page) * c.H + (plane[n] >> 1);
+                u[n] = __ldg(reinterpret_cast<const uint4*>((plane[n] & 1 ? c.v_codes : c.k_codes) + at * bytes +
+                                                           static_cast<int64_t>(w.slot0) * c.D + 16 * static_cast<int64_t>(k[n])));
+                scale[n] = __ldg((plane[n] & 1 ? c.v_scales : c.k_scales) + at);
+            }
 #pragma unroll
-        for (int n = 0; n < kUnroll; ++n) {
-            const int i = i0 + n * kThreads;
-            if (i >= chunks * count) break;
-            const int p = i / chunks, k = i - p * chunks, tok = k / vecs;
-            const uint32_t x[4] = {u[n].x, u[n].y, u[n].z, u[n].w};
-            float f[16];
+            for (int n = 0; n < kUnroll; ++n) {
+                if (i0 + n * kThreads >= chunks * planes) break;
+                const int tok = a.vecs.of(k[n]);
+                const uint32_t x[4] = {u[n].x, u[n].y, u[n].z, u[n].w};
+                float f[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) f[e] = code_value<MODE>(x[e / 4] >> (8 * (e & 3)) & 255u) * scale[n];
-            store(p0 + p, w.row0 + tok, (k - tok * vecs) * 16, f);
+                for (int e = 0; e < 4; ++e) word_values<MODE>(x[e], f + 4 * e);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) f[e] *= scale[n];
+                store(plane[n], w.row0 + tok, (k[n] - tok * vecs) * 16, f);
+            }
         }
     }
 }
@@ -405,10 +474,15 @@ cudaError_t launch_pdl(void (*kernel)(Args...), dim3 grid, int threads, cudaStre
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// Planes a CTA takes: as many as leave about six CTAs for every SM, so that few
-// blocks of tokens are spread over their heads and many amortise the lookup.
-int planes_per_cta(const KvCache& c, int64_t items) {
-    const int64_t runs = (6 * 148 + items - 1) / items;
+// Planes a CTA takes: a block of tokens is cut into runs of planes of at least about
+// 4096 values, into no more than make 1100 CTAs (or three a block). What few tokens cost
+// is the number of CTAs: appending to 128 sequences takes 11 us with one a block, 26 with one a
+// plane; a prompt of 8192 tokens takes 36 us with two planes a CTA, 40 with one or four.
+int planes_per_cta(const KvCache& c, const KvSteps& st, int64_t items) {
+    const int64_t by_values = st.rows * 2 * c.H * c.D / items / 4096;
+    const int64_t by_ctas = 1100 / items > 3 ? 1100 / items : 3;
+    int64_t runs = by_values < by_ctas ? by_values : by_ctas;
+    if (runs < 1) runs = 1;
     const int64_t planes = (2 * c.H + runs - 1) / runs;
     return static_cast<int>(planes < 1 ? 1 : planes);
 }
@@ -418,8 +492,8 @@ int planes_per_cta(const KvCache& c, int64_t items) {
 cudaError_t launch_kv_quantize(const void* k, const void* v, int64_t k_stride, int64_t v_stride, int dt,
                                const KvCache& c, const KvSteps& st, cudaStream_t stream) {
     const int64_t items = kv_items(st.rows, st.S, 1, c.block, 2);
-    const int planes = planes_per_cta(c, items);
-    QuantArgs a{{k, v}, {k_stride, v_stride}, planes, c, st};
+    const int planes = planes_per_cta(c, st, items);
+    QuantArgs a{{k, v}, {k_stride, v_stride}, planes, Divider(c.D / 8), c, st};
     const dim3 grid(static_cast<unsigned>(items), (2 * c.H + planes - 1) / planes, 1);
     if (dt == NV_F32)
         return c.mode == NV_KV_INT8 ? launch_pdl(kv_quantize_kernel<NV_F32, NV_KV_INT8>, grid, kThreads, stream, a)
@@ -431,8 +505,8 @@ cudaError_t launch_kv_quantize(const void* k, const void* v, int64_t k_stride, i
 cudaError_t launch_kv_dequantize(void* k, void* v, int dt, const KvCache& c, const KvSteps& st,
                                  cudaStream_t stream) {
     const int64_t items = kv_items(st.rows, st.S, 1, c.block, 2);
-    const int planes = planes_per_cta(c, items);
-    DequantArgs a{{k, v}, planes, c, st};
+    const int planes = planes_per_cta(c, st, items);
+    DequantArgs a{{k, v}, planes, Divider(c.D / 16), c, st};
     const dim3 grid(static_cast<unsigned>(items), (2 * c.H + planes - 1) / planes, 1);
     if (dt == NV_F32)
         return c.mode == NV_KV_INT8 ? launch_pdl(kv_dequantize_kernel<NV_F32, NV_KV_INT8>, grid, kThreads, stream, a)
