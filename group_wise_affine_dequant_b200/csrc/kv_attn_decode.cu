@@ -135,9 +135,11 @@ kv_attn_decode_kernel(const __grid_constant__ DecodeArgs p, const __grid_constan
     __shared__ BlockScales scales[2][kBlocksMax];
     __shared__ int64_t prefix[kThreads + 1];
     __shared__ float join_m[kConsumers][RT], join_l[kConsumers][RT];
+    __shared__ int failed;  // a consumer's wait gave up: all leave together, at a barrier
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
     if (tid == 0) {
+        failed = 0;
         for (int i = 0; i < NS; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 2);
@@ -343,7 +345,9 @@ kv_attn_decode_kernel(const __grid_constant__ DecodeArgs p, const __grid_constan
         for (int64_t w = blockIdx.x; ok && w < total; w += gridDim.x, ++it) {
             const int slot = it & 1;
             ok = mbar_wait(&meta_full[slot], (it >> 1) & 1, 0x64);
-            if (!ok) break;
+            if (!ok) failed = 1;
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            if (failed) break;
             const ItemMeta& m = meta[slot];
             // queries as B operands: lane 4 g + t4 holds values t4 * D / 4 .. of row g (of each group of 8)
             uint32_t qb[NQ][KS][2];
@@ -412,8 +416,10 @@ kv_attn_decode_kernel(const __grid_constant__ DecodeArgs p, const __grid_constan
             const int stages_here = (m.t1 - m.t0 + kTile - 1) / kTile;
             for (int n_stage = pair; n_stage < stages_here; n_stage += 2) {
                 const int stage = (before + n_stage) % NS;
-                ok = mbar_wait(&full[stage], (before + n_stage) / NS & 1, 0x65);
-                if (!ok) break;
+                if (!mbar_wait(&full[stage], (before + n_stage) / NS & 1, 0x65)) {
+                    failed = 1;
+                    break;
+                }
                 const int j0 = m.t0 + n_stage * kTile + 32 * (warp & 1);
                 const uint8_t* kt = stages + stage * 2 * kHalf + 32 * (warp & 1) * D;
                 const uint8_t* vt = kt + kHalf;
@@ -558,7 +564,6 @@ kv_attn_decode_kernel(const __grid_constant__ DecodeArgs p, const __grid_constan
                 if (lane == 0) mbar_arrive(&empty[stage]);
             }
             before += stages_here;
-            if (!ok) break;
             // join the four warps: references and sums first, then the outputs in warp order
 #pragma unroll
             for (int n = 0; n < NQ; ++n)
@@ -632,6 +637,7 @@ kv_attn_decode_kernel(const __grid_constant__ DecodeArgs p, const __grid_constan
                 }
             }
             asm volatile("bar.sync 1, 128;" ::: "memory");
+            if (failed) break;
             if (lane == 0) mbar_arrive(&meta_empty[slot]);
         }
     }

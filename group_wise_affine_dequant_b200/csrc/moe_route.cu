@@ -305,7 +305,7 @@ __device__ __forceinline__ float key_value(uint32_t key) {
 
 // VPL: experts per lane. 32 * VPL >= E.
 template <int DT, int VPL>
-__global__ void __launch_bounds__(32 * kWarps) moe_route_kernel(const __grid_constant__ RouteArgs a) {
+__global__ void __launch_bounds__(32 * kWarps, VPL <= 8 ? 12 : 1) moe_route_kernel(const __grid_constant__ RouteArgs a) {
     extern __shared__ double route_smem[];  // per warp: E + groups doubles (the fp64 ranking)
     __shared__ int s_sel[kWarps][kMaxTopk];
     constexpr uint32_t kPlace = VPL - 1;     // a key's low bits: kPlace - (place in the lane)
