@@ -6,18 +6,18 @@
 // SM and item; rows form two subtiles of 128 that share every converted key and
 // value tile and take turns on the tensor core: while one subtile's softmax runs, the
 // other's products do.
-//   warp 0           issues the products (the lowest warp: it goes before the others
-//                    when it has an instruction ready): S = Q K^T (K-major operands), O += P V
+//   warp 0           issues the products: S = Q K^T (K-major operands), O += P V
 //                    with P from TMEM and V read along tokens (MN-major), so V
 //                    needs no transpose
 //   warp 1           looks pages and scales up, four tiles at a time, up to eight ahead
-//   warps 2, 3       fill the warpgroup (registers are dealt out by warpgroups)
 //   warps 4-7, 8-11  softmax of subtile 0, 1: thread = row = TMEM lane; scores
 //                    arrive in TMEM, weights go back over them as fp16
-//   warps 12-19      converters: 8-bit codes from global memory (the next tile's
-//                    loads are in flight while this one's are converted), exact
+//   warps 12-15      converters: 8-bit codes from global memory (the next half tile's
+//                    loads are in flight while one is converted), exact
 //                    fp16 into swizzled shared tiles [token][value], a ring of two
 //                    K and two V tiles
+// Sixteen warps leave 128 registers a thread and none spills: with 200 KB of shared memory taken there
+// is next to no L1, and spilled registers would come back from the L2.
 // TMEM (512 columns): S0, S1 (128 each, P over the first 64), O0, O1 (D each).
 //
 // Block scales never touch the tiles: keys' are factors of the scores, values' join
@@ -25,8 +25,11 @@
 // A row's reference follows its running maximum only when that passes it by
 // kSlack, so rescaling O in TMEM is rare and the softmax warps do it themselves.
 //
-// Bound: the tensor core (4 * D flops a pair) together with the exponentials
-// (16 a clock and SM: 128 x 128 scores cost as many clocks as their two products).
+// Bound: neither the tensor core (30 % busy) nor the exponentials (16 a clock and SM, 45 %),
+// but the chain of one subtile's step: its products (1.65 us of cycles at 1 GHz, both
+// subtiles' in turn), then a softmax of 2.9 whose 128 exponentials a thread can issue one in 8
+// cycles at best. Measured and not kept: scores in registers (unrolled), two threads a
+// row, an issuing warp a subtile, a share of the exponentials as polynomials.
 #include <cstdint>
 
 #include "kv_mma.cuh"
@@ -36,13 +39,8 @@ namespace {
 
 constexpr int kRows = 256;     // rows an item
 constexpr int kTile = 128;     // tokens a tile
-constexpr int kIssueWarp = 0, kLookupWarp = 1, kSoftmaxWarp0 = 4, kSoftmaxWarps = 8, kConvertWarp0 = 12, kConvertWarps = 8;
-constexpr int kThreads = 32 * 20;
-// Registers a thread by role: the block starts with kThreads * kRegsLaunch, and the
-// shares must not sum to more (a share that cannot be had would wait forever).
-constexpr int kRegsLaunch = 96, kRegsSoftmax = 136, kRegsConvert = 80, kRegsRest = 48;
-static_assert(32 * kSoftmaxWarps * kRegsSoftmax + 32 * kConvertWarps * kRegsConvert + 128 * kRegsRest <= kThreads * kRegsLaunch, "");
-static_assert(kRegsConvert <= kRegsLaunch && kRegsRest <= kRegsLaunch && kRegsSoftmax >= kRegsLaunch, "dec lowers, inc raises");
+constexpr int kIssueWarp = 0, kLookupWarp = 1, kSoftmaxWarp0 = 4, kSoftmaxWarps = 8, kConvertWarp0 = 12, kConvertWarps = 4;
+constexpr int kThreads = 32 * 16;
 constexpr int kTmemCols = 512;
 constexpr int kMeta = 8;       // ring of per-tile lookups
 constexpr int kMetaBatch = 4;  // tiles looked up at once
@@ -164,7 +162,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
 
     if (tid == 0) {
         for (int i = 0; i < 4; ++i) {
-            mbar_init(&full[i], 32 * kConvertWarps);
+            mbar_init(&full[i], kConvertWarps);
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -237,7 +235,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
 
     if (warp >= kSoftmaxWarp0 && warp < kSoftmaxWarp0 + kSoftmaxWarps) {
         // ------------------------------------------------------------- softmax
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
         const int sub = (warp - kSoftmaxWarp0) >> 2;
         const int r_sub = tid & 127;              // row of the subtile = TMEM lane
         const int row = sub * 128 + r_sub;
@@ -440,69 +437,76 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
         tc::tc_fence_before();
     } else if (warp >= kConvertWarp0) {
         // ---------------------------------------------------------- converters
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConvert));
         const int ct = tid - 32 * kConvertWarp0;
-        constexpr int kVecs = D / 16;                        // 16-byte pieces of codes a token
-        constexpr int kStep = 32 * kConvertWarps / kVecs;    // tokens a pass of all threads
-        constexpr int kPasses = kTile / kStep;               // 4 (D 128) or 2 (D 64)
-        const int vec = ct % kVecs, tok0 = ct / kVecs;
-        // threads of the two halves of 64 values store their two pieces in opposite order: no bank conflicts
-        const int swap = (vec >> 2) & 1;
-        auto load = [&](const uint8_t* codes, int i, uint4 (&raw)[kPasses]) {
-            const int64_t* at = places[i & (kMeta - 1)];
-            const int left = hi - (lo + i * kTile);
+        // A thread takes 16 values (16 bytes of codes, two 16-byte pieces of fp16) of every 16th (32nd) token.
+        // Eight neighbours are two tokens by four such runs of one half of 64 values, whose pieces
+        // fall into different banks; a warp reads whole rows of codes.
+        constexpr int kStep = D == 128 ? 16 : 32;      // tokens a pass of all threads
+        constexpr int kPasses = kTile / 2 / kStep;     // passes of half a tile: 4 (D 128) or 2 (D 64)
+        const int run = lane & 3, half = D == 128 ? lane >> 3 & 1 : 0;
+        const int tok0 = D == 128 ? (ct >> 5) * 4 + (lane >> 4) * 2 + (lane >> 2 & 1) : ct >> 2;
+        const uint32_t at0 = half * L::kHalf + sw128_at(tok0, 2 * run), at1 = half * L::kHalf + sw128_at(tok0, 2 * run + 1);
+        const uint32_t code0 = (tok0 & 15) * D + 64 * half + 16 * run;
+        // codes of tokens 64 part .. of tile i
+        auto load = [&](const uint8_t* codes, int i, int part, uint4 (&raw)[kPasses]) {
+            const int64_t* at = places[i & (kMeta - 1)] + 4 * part + (tok0 >> 4);
+            const int left = hi - (lo + i * kTile) - 64 * part - tok0;
 #pragma unroll
             for (int n = 0; n < kPasses; ++n) {
-                const int r = tok0 + kStep * n;
-                const int64_t o = at[r >> 4];
+                const int64_t o = at[n * (kStep / 16)];
                 raw[n] = make_uint4(0, 0, 0, 0);
-                if (o >= 0 && r < left) raw[n] = __ldg(reinterpret_cast<const uint4*>(codes + o + ((r & 15) * D + 16 * vec)));
+                if (o >= 0 && kStep * n < left) raw[n] = __ldg(reinterpret_cast<const uint4*>(codes + o + code0));
             }
         };
-        auto convert = [&](const uint4 (&raw)[kPasses], uint8_t* tile) {
-            uint8_t* half = tile + (vec >> 2) * L::kHalf;
+        auto convert = [&](const uint4 (&raw)[kPasses], uint8_t* tile, int part) {
+            uint8_t* t0 = tile + at0 + part * (64 * 128);
+            uint8_t* t1 = tile + at1 + part * (64 * 128);
 #pragma unroll
             for (int n = 0; n < kPasses; ++n) {
-                const uint32_t x[4] = {raw[n].x, raw[n].y, raw[n].z, raw[n].w};
-                uint4 y[2];
-#pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    const uint32_t a = prepare_word<MODE>(x[2 * m]), b = prepare_word<MODE>(x[2 * m + 1]);
-                    y[m] = make_uint4(pair_lo_h2<MODE>(a), pair_hi_h2<MODE>(a), pair_lo_h2<MODE>(b), pair_hi_h2<MODE>(b));
-                }
-                const int r = tok0 + kStep * n;
-                *reinterpret_cast<uint4*>(half + sw128_at(r, 2 * (vec & 3) + swap)) = swap ? y[1] : y[0];
-                *reinterpret_cast<uint4*>(half + sw128_at(r, 2 * (vec & 3) + 1 - swap)) = swap ? y[0] : y[1];
+                const uint32_t a = prepare_word<MODE>(raw[n].x), b = prepare_word<MODE>(raw[n].y);
+                const uint32_t c = prepare_word<MODE>(raw[n].z), d = prepare_word<MODE>(raw[n].w);
+                *reinterpret_cast<uint4*>(t0 + n * (kStep * 128)) =
+                    make_uint4(pair_lo_h2<MODE>(a), pair_hi_h2<MODE>(a), pair_lo_h2<MODE>(b), pair_hi_h2<MODE>(b));
+                *reinterpret_cast<uint4*>(t1 + n * (kStep * 128)) =
+                    make_uint4(pair_lo_h2<MODE>(c), pair_hi_h2<MODE>(c), pair_lo_h2<MODE>(d), pair_hi_h2<MODE>(d));
             }
-            fence_proxy_async();
         };
-        uint4 kraw[kPasses], vraw[kPasses];
+        auto done = [&](uint64_t* bar) {
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+        };
+        // halves of K, then of V, the next half's loads in flight while one is converted
+        uint4 even[kPasses], odd[kPasses];
         if (tiles > 0) {
             ok = mbar_wait(&m_full[0], 0, 0x74);
-            if (ok) load(p.c.k_codes, 0, kraw);
+            if (ok) load(p.c.k_codes, 0, 0, even);
         }
         for (int i = 0; ok && i < tiles; ++i) {
-            load(p.c.v_codes, i, vraw);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&m_empty[i & (kMeta - 1)]);
             const int ks = 2 * (i & 1), vs = ks + 1;
             const uint32_t free_parity = ((i >> 1) & 1) ^ 1;
+            load(p.c.k_codes, i, 1, odd);
             ok = mbar_wait(&empty[ks], free_parity, 0x75);
             if (!ok) break;
-            convert(kraw, ring + ks * L::kSub);
-            mbar_arrive(&full[ks]);
+            convert(even, ring + ks * L::kSub, 0);
+            load(p.c.v_codes, i, 0, even);
+            convert(odd, ring + ks * L::kSub, 1);
+            done(&full[ks]);
+            load(p.c.v_codes, i, 1, odd);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&m_empty[i & (kMeta - 1)]);
+            ok = mbar_wait(&empty[vs], free_parity, 0x7C);
+            if (!ok) break;
+            convert(even, ring + vs * L::kSub, 0);
             if (i + 1 < tiles) {
                 ok = mbar_wait(&m_full[(i + 1) & (kMeta - 1)], ((i + 1) / kMeta) & 1, 0x7B);
                 if (!ok) break;
-                load(p.c.k_codes, i + 1, kraw);
+                load(p.c.k_codes, i + 1, 0, even);
             }
-            ok = mbar_wait(&empty[vs], free_parity, 0x7C);
-            if (!ok) break;
-            convert(vraw, ring + vs * L::kSub);
-            mbar_arrive(&full[vs]);
+            convert(odd, ring + vs * L::kSub, 1);
+            done(&full[vs]);
         }
     } else {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
       if (warp == kLookupWarp) {
         // ------------------------------------------------- pages and scales: lane = (tile of four, chunk of 16 tokens)
         const float lg_max = log2f(vmax);
@@ -640,12 +644,6 @@ cudaError_t launch(const PrefillArgs& p, cudaStream_t stream) {
     cudaError_t e = cudaFuncSetAttribute(kv_attn_prefill_kernel<MODE, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          Smem<D>::kBytes);
     if (e != cudaSuccess) return e;
-    // the register shares are taken from what the block is launched with
-    static const int regs = [] {
-        cudaFuncAttributes at{};
-        return cudaFuncGetAttributes(&at, kv_attn_prefill_kernel<MODE, D>) == cudaSuccess ? at.numRegs : 0;
-    }();
-    if (regs < kRegsLaunch) return cudaErrorLaunchOutOfResources;
     // Not launched programmatically: its CTAs take a whole SM each, and early ones only keep the last
     // of the kernel before it from theirs (ragged chunks, behind the kernel for few rows: 335 -> 320 us).
     cudaLaunchAttribute pdl[1];
