@@ -13,6 +13,7 @@
 // and the codes, so they are read once; a few tokens (a decoding step) take one
 // warp a plane, whole blocks the CTA. Bound by memory: 2 bytes in and 1 out per
 // bf16 value, and the reverse for the read-back.
+#include <cfloat>
 #include <cstdint>
 
 #include "kv.cuh"
@@ -278,17 +279,20 @@ __device__ __forceinline__ void quantize_plane(const QuantArgs& a, const BlockWo
     // a tiny scale's reciprocal or remainders would leave the normal range: move both by 2^64, exactly
     const float lift = scale < 8.6736174e-19f ? 18446744073709551616.f : 1.f;  // 2^-60, 2^64
     const float s2 = scale * lift, inv = scale > 0.f ? 1.f / s2 : 0.f;
+    const float edge = fminf(kLargest * scale, FLT_MAX);  // the product may round to infinity
     auto store = [&](const Raw8<DT>& r, int i) {
         uint2 o = make_uint2(0u, 0u);
         if (scale > 0.f) {
             float f[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) f[j] = r.get(j);
-            if (odd) {  // NaN is kept as 0, an infinity as the largest code
+            // NaN is kept as 0, an infinity as the largest code; so is what a subnormal scale, of a few
+            // bits, leaves above it
+            if (odd || lift != 1.f) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     f[j] = f[j] == f[j] ? f[j] : 0.f;
-                    f[j] = fminf(fmaxf(f[j], -kLargest * scale), kLargest * scale);
+                    f[j] = fminf(fmaxf(f[j], -edge), edge);
                 }
             }
             if (lift != 1.f) {

@@ -276,3 +276,23 @@ def test_refusals():
     with pytest.raises(nvq.NvqError):
         nvq.nv_kv_dequantize(kc, ks, kc, ks, *d, rows=4, dtype=torch.float16)
     assert nvq.nv_kv_dequantize(kc, ks, kc, ks, *d, rows=0)[0].shape == (0, 2, 64)
+
+
+@pytest.mark.parametrize("mode", ["int8", "e4m3"])
+def test_the_ends_of_the_fp32_range(mode):
+    """Blocks whose scale is a subnormal of a few bits, so that their largest value lies above the
+    largest code times it, and an infinity beside the largest float, whose code times scale overflows."""
+    D, H, block = 32, 1, 16
+    units = [1, 63, 64, 127, 190, 191, 254, 300, 700, 1000, 5000, 16065, 40000, 100000]
+    step = R.Step([16 * (len(units) + 2)], [16 * (len(units) + 2)], block, seed=4)
+    x = torch.zeros(step.rows, 3 * H, D)
+    g = torch.Generator().manual_seed(2)
+    for i, n in enumerate(units):
+        share = torch.randint(-n, n + 1, (16, 3 * H, D), generator=g)
+        share[3, :, 5], share[4, :, 6] = n, -n
+        x[16 * i: 16 * i + 16] = (share.double() * 2.0 ** -149).float()
+    most = torch.finfo(F32).max
+    x[-32:] = torch.randn(32, 3 * H, D, generator=g) * 1e37
+    x[-30, :, 3], x[-29, :, 4] = most, float("inf")
+    x[-12, :, 3], x[-11, :, 4] = -most, float("-inf")
+    _write_case(step, H, D, mode, F32, 50, x=x)
