@@ -251,7 +251,8 @@ kv_attn_decode_kernel(const __grid_constant__ DecodeArgs p, const __grid_constan
                 const int b = lane + 32 * i;
                 vs_of[i] = 0.f;
                 if (b < blocks) {
-                    const int page = page_of(p.st, p.c, s, block0 + b);
+                    // blocks in front of every row's window only share a stage with those in it
+                    const int page = (block0 + b + 1) * p.c.block > lo_min ? page_of(p.st, p.c, s, block0 + b) : -1;
                     float ks = -1.f;
                     if (page >= 0) {
                         const int64_t ph = static_cast<int64_t>(page) * p.c.H + h;

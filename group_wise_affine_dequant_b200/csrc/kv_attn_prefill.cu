@@ -200,6 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
         hi = p1 + 1 < hi ? p1 + 1 : hi;
         if (p.a.window > 0 && p0 + 1 > p.a.window) lo = p0 + 1 - p.a.window;
     }
+    const int lo_seen = lo;  // what is in front of it only shares a tile with what the window shows
     lo = lo / kTile * kTile;
     int tiles = hi > lo ? (hi - lo + kTile - 1) / kTile : 0;
     if (p.splits > 1) {
@@ -213,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
 
     // ---- the largest value scale of the item: weights carry value scales relative to it
     if (tiles > 0) {
-        const int b0 = lo / p.c.block, b1 = (hi - 1) / p.c.block;
+        const int b0 = (lo > lo_seen ? lo : lo_seen) / p.c.block, b1 = (hi - 1) / p.c.block;
         float most = 0.f;
         for (int b = b0 + tid; b <= b1; b += kThreads) {
             const int32_t page = __ldg(p.st.pages + static_cast<int64_t>(s) * p.st.max_pages + b);
@@ -517,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
             const int j = lo + i * kTile + 16 * c;
             ChunkScales t{-1.f, 0.f, 1.f, 0.f};
             int64_t at = -1;
-            if (i < tiles && j < hi) {
+            if (i < tiles && j < hi && j + 16 > lo_seen) {
                 const int b = j / p.c.block;
                 const int page = page_of(p.st, p.c, s, b);
                 if (page >= 0) {

@@ -424,7 +424,8 @@ size_t nv_kv_attention_workspace_size(nv_dtype dt, int64_t rows, int Hq, int H, 
  * Attention of a step's queries over the cache. Query head i reads key/value
  * head i / (Hq / H); the row of sequence s at place p (its last row is at
  * lens[s] - 1) sees token j if j < lens[s], and
- *   causal = 1: j <= p, and j > p - window if window > 0;
+ *   causal = 1: j <= p, and j > p - window if window > 0 (pages in front of the
+ *       windows of all of a sequence's rows may be given back: they are not asked for);
  *   causal = 0: every token (window must be 0), as for an encoder's states.
  *   out = sum_j softmax_j(scale * q . k_j) v_j, k and v as nv_kv_dequantize gives
  *   them in fp32.

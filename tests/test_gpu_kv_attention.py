@@ -296,3 +296,30 @@ def test_refusals():
         with pytest.raises(ValueError):
             nvq.nv_kv_attention(a["q"], a["kc"], ks, a["kc"], ks, *d, out=a["out"])
     assert nvq.nv_kv_attention(q[:0], kc, ks, kc, ks, *d).shape == (0, 4, 64)
+
+
+@pytest.mark.parametrize("dtype,D", [(BF16, 128), (BF16, 64), (F32, 64)])
+@pytest.mark.parametrize("news", [1, 70])
+@pytest.mark.parametrize("block", [16, 128])
+def test_pages_in_front_of_a_window_are_free(dtype, D, news, block):
+    """A sliding window's pages in front of every row's first visible token may be given back: their
+    entries are not asked for, nor is what they point to read."""
+    H, G, window, mode = 2, 4, 100, "e4m3"
+    lens = [700, 333]
+    step = R.Step(lens, [news, 1], block, seed=11)
+    caches = (*_cache(step.P, H, block, D, mode, 1), *_cache(step.P, H, block, D, mode, 2))
+    q = torch.randn(step.rows, H * G, D, generator=torch.Generator().manual_seed(3)).to(dtype)
+    out, *terms = R.attention(q, *caches, step, mode, D ** -0.5, True, window)
+    room = R.attention_tolerance(out, terms, dtype, D, max(lens))
+    free = [max(n - m + 1 - window, 0) // block for n, m in zip(lens, step.news)]
+    dead = torch.cat([step.pages[s, : free[s]] for s in range(2)]).long()
+    assert len(dead) > 0
+    for raw, sc in ((caches[0], caches[1]), (caches[2], caches[3])):
+        raw[dead] = 0x7F
+        sc[dead] = float("nan")
+    got = _run(step, q, caches, mode, causal=True, window=window, max_q=news)
+    assert bool(((got.double() - out).abs() <= room).all())
+    for s in range(2):
+        step.pages[s, : free[s]] = -1
+    got = _run(step, q, caches, mode, causal=True, window=window, max_q=news)
+    assert bool(((got.double() - out).abs() <= room).all())
