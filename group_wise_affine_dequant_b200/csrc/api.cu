@@ -423,7 +423,7 @@ nv_status nv_kv_attention(const void* q, int64_t q_stride, nv_dtype dt, int64_t 
     nv_status st = check_kv(dt, rows, c, S, max_pages, &empty);
     if (st != NV_OK) return st;
     if (Hq < 1 || Hq > 65536 || Hq % H || window < 0 || (window > 0 && !causal) || max_q < 0 ||
-        rows * Hq > 0x7FFFFFFF)
+        rows * Hq > 0x7FFFFFFF || S * H > 0x7FFFFFF)  // the grids and partials of every kernel stay in 32 bits
         return NV_ERR_INVALID_ARG;
     const size_t need = nv_kv_attention_workspace_size(dt, rows, Hq, H, block, D, max_pages, S, max_q);
     if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return NV_ERR_WORKSPACE;

@@ -35,6 +35,9 @@ struct KvSteps {
     uint32_t* flags;  // may be null
 };
 
+// Places are 32-bit; the rest is room for a chunk's or tile's end behind them.
+constexpr int kMaxLen = 0x7FFF0000;
+
 struct SeqSpan {
     int64_t row0;  // first row of the step
     int n;         // rows
@@ -54,7 +57,7 @@ __device__ __forceinline__ SeqSpan seq_span(const KvSteps& st, int s, int block)
     const int64_t r1 = clamped_start(st, s + 1);
     r.n = r1 > r.row0 ? static_cast<int>(r1 - r.row0) : 0;
     const int64_t room = st.max_pages * block;
-    const int64_t cap = room < 0x7FFFFF00 ? room : 0x7FFFFF00;  // places are 32-bit
+    const int64_t cap = room < kMaxLen ? room : kMaxLen;
     r.len = l0 < 0 ? 0 : l0 > cap ? static_cast<int>(cap) : l0;
     r.first = r.len - r.n;
     if (st.flags && (a0 < 0 || a1 < a0 || a1 > st.rows || l0 < 0 || l0 > cap || r.n > r.len))
@@ -150,12 +153,17 @@ struct KvDecodeSizes {
     bool only;
     int64_t G, most_rows;  // heads of a group; most flattened rows a sequence has
 };
+// Bytes of the partial outputs and log-sums of `rows` rows, at most 2^50: no workspace holds those, so
+// that such a call is refused, and the sizes of two kernels add up without wrapping around.
+inline size_t kv_part_bytes(int64_t rows, int64_t parts, int D) {
+    constexpr size_t kMost = static_cast<size_t>(1) << 50;
+    const size_t row = static_cast<size_t>(parts) * (D + 1) * sizeof(float);
+    return static_cast<size_t>(rows) > kMost / row ? kMost : static_cast<size_t>(rows) * row;
+}
 struct KvDecodePlan {
     int target, max_chunks, tile_rows, row_limit;
     int64_t part_rows;
-    size_t bytes(int D) const {
-        return max_chunks > 1 ? static_cast<size_t>(part_rows) * max_chunks * (D + 1) * sizeof(float) : 0;
-    }
+    size_t bytes(int D) const { return max_chunks > 1 ? kv_part_bytes(part_rows, max_chunks, D) : 0; }
 };
 KvDecodePlan kv_decode_plan(const KvDecodeSizes& z, int num_sms);
 cudaError_t launch_kv_attn_decode(const KvAttn& a, const KvCache& c, const KvSteps& st, const KvDecodePlan& plan,
@@ -171,9 +179,7 @@ struct KvPrefillSizes {
 struct KvPrefillPlan {
     int64_t items;
     int splits;
-    size_t bytes(int64_t rows, int Hq, int D) const {
-        return splits > 1 ? static_cast<size_t>(rows) * Hq * splits * (D + 1) * sizeof(float) : 0;
-    }
+    size_t bytes(int64_t rows, int Hq, int D) const { return splits > 1 ? kv_part_bytes(rows * Hq, splits, D) : 0; }
 };
 KvPrefillPlan kv_prefill_plan(const KvPrefillSizes& z, int num_sms);
 cudaError_t launch_kv_attn_prefill(const KvAttn& a, const KvCache& c, const KvSteps& st, const KvPrefillPlan& plan,

@@ -762,7 +762,7 @@ KvDecodePlan kv_decode_plan(const KvDecodeSizes& z, int num_sms) {
     const int64_t groups = z.S * z.H;
     int64_t target = (2 * kCtas * static_cast<int64_t>(num_sms) + groups - 1) / groups;
     r.target = static_cast<int>(target < 1 ? 1 : target > 1 << 20 ? 1 << 20 : target);
-    const int64_t cap = z.max_pages * z.block;  // no sequence is longer
+    const int64_t room = z.max_pages * z.block, cap = room < kMaxLen ? room : kMaxLen;  // no sequence is longer
     // chunks grow with the span, so the most there are is where the minimum or the maximum length binds
     int64_t most = (cap + kChunkMax - 1) / kChunkMax;
     const int64_t by_min = (cap + kChunkMin - 1) / kChunkMin;

@@ -362,7 +362,8 @@ nv_status nv_moe_route(const void* logits, nv_dtype dt, int64_t T, int64_t E, co
  * A page is a block of `block` tokens (16, 32, 64 or 128) of H heads of D
  * values (a multiple of 16 up to 256).
  * The step descriptor, shared by the three calls (int32 device arrays):
- *   lens    [S]: tokens of each sequence, this step's included;
+ *   lens    [S]: tokens of each sequence, this step's included; at most max_pages * block and
+ *           2^31 - 2^16 (what is longer is flagged and cut);
  *   starts  [S + 1]: ascending; rows starts[s] .. starts[s + 1] - 1 of the step
  *           are the LAST tokens of sequence s, in order (none is allowed);
  *   pages   [S, max_pages]: block j of sequence s is page pages[s, j]. Only
@@ -433,7 +434,8 @@ size_t nv_kv_attention_workspace_size(nv_dtype dt, int64_t rows, int Hq, int H, 
  * before, on the same stream). A row that sees nothing gives zeros; tokens of
  * a page out of range are not seen.
  * q       [rows, Hq, D] in `dt` (NV_F32 or NV_BF16), rows q_stride elements apart
- *         (as k_stride above); out [rows, Hq, D] dense in `dt`. Hq a multiple of H.
+ *         (as k_stride above); out [rows, Hq, D] dense in `dt`. Hq a multiple of H, at most 65536;
+ *         rows * Hq below 2^31, S * H at most 2^27 - 1.
  *         q must be finite: a row that holds NaN or infinities gives no number
  *         and changes no other row.
  * max_q   the largest number of rows of one sequence if known, else 0: a hint

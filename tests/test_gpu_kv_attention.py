@@ -323,3 +323,39 @@ def test_pages_in_front_of_a_window_are_free(dtype, D, news, block):
         step.pages[s, : free[s]] = -1
     got = _run(step, q, caches, mode, causal=True, window=window, max_q=news)
     assert bool(((got.double() - out).abs() <= room).all())
+
+
+@pytest.mark.parametrize("news", [1, 17])
+def test_the_longest_sequence(news):
+    """2^31 - 2^16 tokens in two pages that the table repeats, the second from three quarters on: a
+    softmax over two blocks whose weights carry counts. A longer length is cut and flagged.
+    Tolerance: sums take 64 additions a chunk of 1024 tokens and 2^31 / 2^14 joins (few rows), or
+    2^31 / 16 / 148 (many: 148 parts of the tokens, 16 a product); a product's sum may be cut, not rounded
+    (2^-23 a step where a rounded one costs 2^-24), so half as many steps are added."""
+    H, D, block, mode = 1, 64, 128, "int8"
+    most = 2 ** 31 - 2 ** 16
+    raw, sc = _cache(2, H, block, D, mode, 5)
+    vraw, vs = _cache(2, H, block, D, mode, 6)
+    blocks = most // block
+    border = blocks * 3 // 4
+    pages = torch.zeros(1, blocks + 1, dtype=torch.int32)
+    pages[0, border:] = 1
+    q = torch.randn(news, 1, D, generator=torch.Generator().manual_seed(1)).to(BF16)
+    values = R.code_values(mode)
+    k, v = (values[r.long()][:, 0] * s.double()[:, :, None] for r, s in ((raw, sc), (vraw, vs)))  # [2, block, D]
+    z = torch.einsum("nd,pjd->npj", q[:, 0].double(), k) * D ** -0.5
+    e = torch.exp(z - z.amax((1, 2), keepdim=True)) * torch.tensor([border, blocks - border], dtype=torch.float64)[:, None]
+    p = e / e.sum((1, 2), keepdim=True)
+    want, a = torch.einsum("npj,pjd->nd", p, v), torch.einsum("npj,pjd->nd", p, v.abs())
+    dz = torch.einsum("nd,pjd->npj", q[:, 0].double().abs(), k.abs()).amax((1, 2))[:, None] * D ** -0.5
+    steps = 64 + 2 ** 31 / 2 ** 14 if news == 1 else 2 ** 31 / 16 / 148
+    room = R.attention_tolerance(want, (a, dz, torch.zeros(())), BF16, D, 16 * 1.5 * steps)
+    dev = [raw.view(torch.int8).cuda(), sc.cuda(), vraw.view(torch.int8).cuda(), vs.cuda(), pages.cuda(),
+           torch.tensor([0, news], dtype=torch.int32, device="cuda")]
+    flags = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for length, flag in ((most, 0), (2 ** 31 - 1, R.LENGTH_FLAG)):
+        lens = torch.tensor([length], dtype=torch.int32, device="cuda")
+        got = nvq.nv_kv_attention(q.cuda(), *dev, lens, causal=False, max_q=news, flags=flags).cpu()[:, 0]
+        assert int(flags) == flag and nvq.nv_pipeline_error() == 0
+        err = (got.double() - want).abs()
+        assert bool((err <= room).all()), float((err / room).max())

@@ -95,3 +95,13 @@ def test_attention_workspace():
             assert _attention(**kw, ws=24) == WORKSPACE
     for bad in (dict(H=0), dict(Hq=0), dict(D=0), dict(block=0), dict(rows=-1), dict(S=-1), dict(max_pages=-1)):
         assert _workspace(**bad) == 0
+
+
+def test_attention_of_sizes_that_no_memory_holds():
+    """Products of the largest sizes neither wrap around in the workspace's bytes nor in a grid."""
+    huge = dict(rows=(1 << 31) // 8 - 1, S=(1 << 24) - 1, H=8, max_pages=(1 << 31) - 1, block=128, P=8, max_q=0)
+    assert _workspace(**huge) >= 1 << 50
+    assert _attention(**huge, ws_bytes=1 << 49) == WORKSPACE
+    wide = dict(rows=4, S=(1 << 24) - 1, H=64, Hq=64, q_stride=64 * 128, max_q=0, max_pages=1)
+    assert _attention(**wide, ws_bytes=1 << 62) == INVALID
+    assert _attention(**{**wide, "S": 1 << 20}, q=8, ws_bytes=1 << 62) == INVALID  # the queries' alignment, past the sizes
