@@ -487,7 +487,8 @@ _CALLS = None
 def _calls():
     """The extension module that marshals the calls below (csrc/torch_calls.cpp), bound to
     the loaded library; built first if it is missing. It raises ValueError for tensors
-    that do not fit and returns the outputs, or the status of a refused call."""
+    that do not fit and returns the outputs, or the status of a refused call. Where a
+    stream is given, outputs and workspaces are allocated on it, as under torch.cuda.stream."""
     global _CALLS
     if _CALLS is None:
         L = lib()

@@ -1,7 +1,8 @@
 // The serving calls from torch tensors: the argument marshalling that binding.py
 // does for the other entry points, in C++. A decoding step makes these calls for every layer
 // on sizes where the kernels take a few microseconds; through ctypes and tensor
-// attributes the marshalling alone took 7 to 20 (router 12 us a call, now 6).
+// attributes the marshalling alone took 7 to 20 (one token through the router: 12 us a call,
+// 4.5 so).
 //
 // A Python extension module `_calls` with no logic of its own: it checks what
 // needs shapes, allocates outputs and workspaces, and calls libnvq's C entry
@@ -59,18 +60,23 @@ nv_dtype dtype_of(at::ScalarType t) {
 void need(bool ok, const char* what) {
     if (!ok) throw BadArgument(what);
 }
-// The stream handle that the caller gave, or the device's current stream.
-nv_stream_t stream_of(PyObject* o, c10::DeviceIndex device) {
-    if (o == Py_None) return reinterpret_cast<nv_stream_t>(c10::cuda::getCurrentCUDAStream(device).stream());
-    void* p = PyLong_AsVoidPtr(o);
-    if (!p && PyErr_Occurred()) throw PythonError();
-    return static_cast<nv_stream_t>(p);
-}
-// Makes a device current for a call, where it is not.
+// Makes a device current for a call, where it is not, and with it the stream whose handle the
+// caller gave: outputs and workspaces come from that stream's memory, so that none of them is what
+// another stream still uses, or may take when the call has returned.
 struct On {
-    c10::cuda::OptionalCUDAGuard guard;
-    explicit On(c10::DeviceIndex device) {
-        if (device != c10::cuda::current_device()) guard.set_index(device);
+    c10::cuda::OptionalCUDAGuard on_device;
+    c10::cuda::OptionalCUDAStreamGuard on_stream;
+    nv_stream_t stream;
+    On(c10::DeviceIndex device, PyObject* handle) {
+        if (handle == Py_None) {
+            if (device != c10::cuda::current_device()) on_device.set_index(device);
+            stream = reinterpret_cast<nv_stream_t>(c10::cuda::getCurrentCUDAStream(device).stream());
+            return;
+        }
+        void* p = PyLong_AsVoidPtr(handle);
+        if (!p && PyErr_Occurred()) throw PythonError();
+        stream = static_cast<nv_stream_t>(p);
+        on_stream.reset_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(p), device));
     }
 };
 at::Tensor fresh(at::IntArrayRef shape, at::ScalarType t, c10::DeviceIndex device) {
@@ -152,9 +158,9 @@ PyObject* moe_route(PyObject*, PyObject* const* a, Py_ssize_t n) {
                  "bias must be contiguous fp32 [E] on the logits' device");
             bias = static_cast<const float*>(b.data_ptr());
         }
-        const On guard(device);
+        const On on(device, a[11]);
         auto output = [&](PyObject* o, at::ScalarType t, const char* what) {
-            if (o == Py_None) return fresh({T, topk < 0 ? 0 : topk}, t, device);
+            if (o == Py_None) return fresh({T, topk < 0 || topk > E ? 0 : topk}, t, device);  // 0: about to be refused
             const at::Tensor& x = tensor(o, what);
             need(is_on(x, device) && x.scalar_type() == t && x.dim() == 2 && x.size(0) == T && x.size(1) == topk &&
                      x.is_contiguous(),
@@ -165,7 +171,7 @@ PyObject* moe_route(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const nv_status st = p_moe_route(z.data_ptr(), dtype_of(z.scalar_type()), T, E, bias, small(a[2]), small(a[4]),
                                          small(a[5]), small(a[6]), topk, small(a[7]), real(a[8]),
                                          static_cast<uint32_t*>(ids.data_ptr()), static_cast<float*>(weights.data_ptr()),
-                                         stream_of(a[11], device));
+                                         on.stream);
         return st == NV_OK ? pair(ids, weights) : refused(st);
     });
 }
@@ -246,11 +252,11 @@ PyObject* kv_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const Cache c(a + 2);
         const int64_t ks = c.stride(k, c.H), vs = c.stride(v, c.H);
         need(k.sizes() == v.sizes() && k.scalar_type() == v.scalar_type(), "k and v must be alike");
-        const On guard(c.device);
+        const On on(c.device, a[10]);
         return refused(p_kv_quantize(k.data_ptr(), v.data_ptr(), ks, vs, dtype_of(k.scalar_type()), k.size(0), c.k_codes,
                                      c.k_scales, c.v_codes, c.v_scales, c.mode, c.P, static_cast<int>(c.H),
                                      static_cast<int>(c.block), static_cast<int>(c.D), c.pages, c.max_pages, c.starts,
-                                     c.lens, c.S, c.flags, stream_of(a[10], c.device)));
+                                     c.lens, c.S, c.flags, on.stream));
     });
 }
 
@@ -263,7 +269,7 @@ PyObject* kv_dequantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
         need(dt != nullptr, "dtype must be a torch.dtype");
         const at::ScalarType type = dt->scalar_type;
         need(rows >= 0, "rows must not be negative");
-        const On guard(c.device);
+        const On on(c.device, a[12]);
         auto output = [&](PyObject* o) {
             if (o == Py_None) return fresh({rows, c.H, c.D}, type, c.device);
             const at::Tensor& x = tensor(o, "out");
@@ -276,7 +282,7 @@ PyObject* kv_dequantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const nv_status st = p_kv_dequantize(c.k_codes, c.k_scales, c.v_codes, c.v_scales, c.mode, c.P,
                                              static_cast<int>(c.H), static_cast<int>(c.block), static_cast<int>(c.D),
                                              c.pages, c.max_pages, c.starts, c.lens, c.S, dtype_of(type), rows,
-                                             k.data_ptr(), v.data_ptr(), c.flags, stream_of(a[12], c.device));
+                                             k.data_ptr(), v.data_ptr(), c.flags, on.stream);
         return st == NV_OK ? pair(k, v) : refused(st);
     });
 }
@@ -294,7 +300,7 @@ PyObject* kv_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int window = small(a[11]);
         const int64_t max_q = integer(a[12]);
         const int H = static_cast<int>(c.H), block = static_cast<int>(c.block), D = static_cast<int>(c.D);
-        const On guard(c.device);
+        const On on(c.device, a[15]);
         at::Tensor out;
         if (a[14] == Py_None) {
             out = fresh({rows, Hq, c.D}, q.scalar_type(), c.device);
@@ -316,7 +322,7 @@ PyObject* kv_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
             q.data_ptr(), qs, dt, rows, static_cast<int>(Hq), c.k_codes, c.k_scales, c.v_codes, c.v_scales, c.mode, c.P, H,
             block, D, c.pages, c.max_pages, c.starts, c.lens, c.S, scale, small(a[10]), window, max_q,
             workspace.defined() ? workspace.data_ptr() : nullptr, workspace.defined() ? workspace.nbytes() : 0,
-            out.data_ptr(), c.flags, stream_of(a[15], c.device));
+            out.data_ptr(), c.flags, on.stream);
         return st == NV_OK ? THPVariable_Wrap(out) : refused(st);
     });
 }

@@ -359,3 +359,28 @@ def test_the_longest_sequence(news):
         assert int(flags) == flag and nvq.nv_pipeline_error() == 0
         err = (got.double() - want).abs()
         assert bool((err <= room).all()), float((err / room).max())
+
+
+@pytest.mark.parametrize("news", [1, 40])
+def test_a_given_stream_owns_the_memory_of_its_call(news):
+    """While a call waits on a side stream, memory that the current stream allocates is not the call's workspace."""
+    H, G, D, mode = 2, 4, 128, "int8"
+    step = R.Step([30000], [news], 64, seed=12)
+    caches = (*_cache(step.P, H, 64, D, mode, 1), *_cache(step.P, H, 64, D, mode, 2))
+    q = torch.randn(step.rows, H * G, D, generator=torch.Generator().manual_seed(1)).to(BF16)
+    want = _run(step, q, caches, mode, max_q=news)
+    dev = [t.cuda() for t in (q, caches[0].view(torch.int8), caches[1], caches[2].view(torch.int8), caches[3], *step.dev())]
+    need = nvq.nv_kv_attention_workspace_size(step.rows, H * G, H, 64, D, step.pages.shape[1], 1, news)
+    assert need > 0
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)  # about 10 ms
+    got = nvq.nv_kv_attention(*dev, max_q=news, stream=side)
+    mine = [torch.full((need,), 7, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    torch.cuda.synchronize()
+    assert all(bool((m == 7).all()) for m in mine) and torch.equal(got.cpu(), want)
+    ids = nvq.nv_moe_route(torch.randn(64, 16, device="cuda"), 2, stream=side)[0]
+    back = nvq.nv_kv_dequantize(*dev[1:], rows=step.rows, stream=side.cuda_stream)
+    side.synchronize()
+    assert ids.shape == (64, 2) and torch.equal(back[0], nvq.nv_kv_dequantize(*dev[1:], rows=step.rows)[0])

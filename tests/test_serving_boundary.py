@@ -1,6 +1,7 @@
 """Argument errors of the router and the key/value cache calls (CPU only: every
 call here is refused, or has nothing to do, before anything is launched)."""
 import pytest
+import torch
 
 import group_wise_affine_dequant_b200 as nvq
 from group_wise_affine_dequant_b200 import binding as B
@@ -105,3 +106,17 @@ def test_attention_of_sizes_that_no_memory_holds():
     wide = dict(rows=4, S=(1 << 24) - 1, H=64, Hq=64, q_stride=64 * 128, max_q=0, max_pages=1)
     assert _attention(**wide, ws_bytes=1 << 62) == INVALID
     assert _attention(**{**wide, "S": 1 << 20}, q=8, ws_bytes=1 << 62) == INVALID  # the queries' alignment, past the sizes
+
+
+def test_tensors_that_do_not_fit():
+    """The Python calls refuse what is not on a GPU, or no tensor, before anything is launched."""
+    z = torch.zeros(4, 8)
+    cache = [torch.zeros(3, 2, 16, 64, dtype=torch.int8), torch.zeros(3, 2)] * 2
+    steps = [torch.zeros(1, 3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)]
+    x = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
+    for bad in (lambda: nvq.nv_moe_route(z, 2), lambda: nvq.nv_moe_route(None, 2), lambda: nvq.nv_moe_route(z, 2, "relu"),
+                lambda: nvq.nv_kv_quantize(x, x, *cache, *steps), lambda: nvq.nv_kv_quantize(x, None, *cache, *steps),
+                lambda: nvq.nv_kv_dequantize(*cache, *steps, rows=4), lambda: nvq.nv_kv_attention(x, *cache, *steps),
+                lambda: nvq.nv_kv_attention(x, 5, *cache[1:], *steps)):
+        with pytest.raises(ValueError):
+            bad()
