@@ -69,7 +69,9 @@ nv_status check_kv_pointers(const nvq::KvCache& c, const nvq::KvSteps& st) {
 }
 // Which attention kernels a call takes, and their workspaces: a pure function of
 // the sizes. bf16 heads of 64 or 128 values have the tensor-core kernels: one for
-// sequences of at most 16 flattened rows (new tokens times heads of the group), one for more.
+// sequences of at most 16 flattened rows (new tokens times heads of the group), one for more
+// (64 sequences of 8192 tokens, 8 heads of 128 values: at 16 rows 355 us and 440, at 20 rows,
+// two tiles of the first, 710 and 440).
 // A call whose sequences may be of both kinds launches both, each leaves the other's alone.
 struct KvAttnPlan {
     bool decode = false, prefill = false;

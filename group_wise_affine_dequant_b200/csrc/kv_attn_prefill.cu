@@ -5,17 +5,20 @@
 // query head of the group)) against its visible tokens, 128 at a time. One CTA per
 // SM and item; rows form two subtiles of 128 that share every converted key and
 // value tile and take turns on the tensor core: while one subtile's softmax runs, the
-// other's products do.
+// other's products do. An item of at most 128 rows (a few tokens of many heads, a prompt's
+// end) is one subtile: both softmax groups hold it, each takes every other tile of
+// tokens, and they join at the end (64 sequences of 8192, 20 rows a head: 700 us with the
+// second group idle, 440 so; as two tiles of the kernel for few rows, 710).
 //   warp 0           issues the products: S = Q K^T (K-major operands), O += P V
 //                    with P from TMEM and V read along tokens (MN-major), so V
 //                    needs no transpose
-//   warp 1           looks pages and scales up, four tiles at a time, up to eight ahead
+//   warp 1           looks pages and scales up, four tiles at a time, up to eight ahead, and
+//                    asks the L2 for their codes
 //   warps 4-7, 8-11  softmax of subtile 0, 1: thread = row = TMEM lane; scores
 //                    arrive in TMEM, weights go back over them as fp16
-//   warps 12-15      converters: 8-bit codes from global memory (the next half tile's
-//                    loads are in flight while one is converted), exact
-//                    fp16 into swizzled shared tiles [token][value], a ring of two
-//                    K and two V tiles
+//   warps 12-15      converters: 8-bit codes from global memory (a tile of them in
+//                    flight in registers), exact fp16 into swizzled shared tiles
+//                    [token][value], a ring of two K and two V tiles
 // Sixteen warps leave 128 registers a thread and none spills: with 200 KB of shared memory taken there
 // is next to no L1, and spilled registers would come back from the L2.
 // TMEM (512 columns): S0, S1 (128 each, P over the first 64), O0, O1 (D each).
@@ -135,6 +138,10 @@ __device__ __forceinline__ uint32_t sw128_at(int r, int piece) {
     return static_cast<uint32_t>((r >> 3) * 1024 + (r & 7) * 128 + ((piece ^ (r & 7)) << 4));
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
 // What a 16-token chunk's scores are multiplied by: positive even where keys or
 // queries are all zero, so that a score of -infinity (not seen) stays one.
 __device__ __forceinline__ float score_factor(float zc, float ks) { return fmaxf(zc * ks, 1e-37f); }
@@ -162,24 +169,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
     __shared__ uint32_t tmem_slot, vmax_bits;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
-    if (tid == 0) {
-        for (int i = 0; i < 4; ++i) {
-            mbar_init(&full[i], kConvertWarps);
-            mbar_init(&empty[i], 1);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&q_full[i], 128);
-            mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], 128);
-            mbar_init(&o_full[i], 1);
-        }
-        for (int i = 0; i < kMeta; ++i) {
-            mbar_init(&m_full[i], 1);
-            mbar_init(&m_empty[i], kSoftmaxWarps + kConvertWarps);
-        }
-        mbar_init_fence();
-        vmax_bits = 0;
-    }
     pdl_launch_dependents();
     pdl_wait();
 
@@ -194,6 +183,27 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
     if (j_item < 0 || j_item * kRows >= seq_rows || seq_rows <= p.row_min) return;
     const int f0 = static_cast<int>(j_item * kRows);
     const int rows = seq_rows - f0 < kRows ? static_cast<int>(seq_rows - f0) : kRows;
+    // One subtile of rows: both softmax groups take it, each every other tile of tokens, and join at the end.
+    const bool alternate = rows <= kRows / 2;
+    const int turns = alternate ? 2 : 1;  // tiles from one of a group's to its next
+    if (tid == 0) {
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&full[i], kConvertWarps);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&q_full[i], 128);
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 128);
+            mbar_init(&o_full[i], 1);
+        }
+        for (int i = 0; i < kMeta; ++i) {
+            mbar_init(&m_full[i], 1);
+            mbar_init(&m_empty[i], (alternate ? kSoftmaxWarps / 2 : kSoftmaxWarps) + kConvertWarps);
+        }
+        mbar_init_fence();
+        vmax_bits = 0;
+    }
     int lo = 0, hi = span.len;
     if (p.a.causal) {
         const int p0 = span.first + f0 / G, p1 = span.first + (f0 + rows - 1) / G;
@@ -240,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
         // ------------------------------------------------------------- softmax
         const int sub = (warp - kSoftmaxWarp0) >> 2;
         const int r_sub = tid & 127;              // row of the subtile = TMEM lane
-        const int row = sub * 128 + r_sub;
+        const int row = alternate ? r_sub : sub * 128 + r_sub;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t s_at = tmem + lanes + static_cast<uint32_t>(sub * 128);
         const uint32_t o_at = tmem + lanes + 256u + static_cast<uint32_t>(sub * D);
@@ -290,10 +300,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
             mbar_arrive(&q_full[sub]);
         }
         float ref = -INFINITY, l = 0.f;
-        for (int i = 0; ok && i < tiles; ++i) {
+        const int first = alternate ? sub : 0;
+        for (int i = first, n = 0; ok && i < tiles; i += turns, ++n) {
             const int j0 = lo + i * kTile;
             const int ms = i & (kMeta - 1);
-            ok = mbar_wait(&m_full[ms], (i / kMeta) & 1, 0x71) && mbar_wait(&s_full[sub], i & 1, 0x72);
+            ok = mbar_wait(&m_full[ms], (i / kMeta) & 1, 0x71) && mbar_wait(&s_full[sub], n & 1, 0x72);
             if (!ok) break;
             tc::tc_fence_after();
             const ChunkScales* ts = scales[ms];
@@ -346,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
                 const float fct = up ? exp2f(ref - mx) : 1.f;
                 ref = up ? mx : ref;
                 l *= fct;
-                if (i > 0) {
+                if (n > 0) {
 #pragma unroll 1
                     for (int c = 0; c < D / 16; ++c) {
                         uint32_t ov[16];
@@ -399,18 +410,57 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
             if (lane == 0) mbar_arrive(&m_empty[ms]);
         }
         // ---- output
-        if (ok && tiles > 0) ok = mbar_wait(&o_full[sub], 0, 0x73);
+        const bool has_o = first < tiles;
+        if (ok && has_o) ok = mbar_wait(&o_full[sub], 0, 0x73);
         tc::tc_fence_after();
-        if (ok) {
+        float4* other = reinterpret_cast<float4*>(ring);  // [D / 4][128]: what the second group found, then its reference and sum
+        float f_own = 1.f, f_other = 0.f;
+        if (alternate && tiles > 1) {
+            float2* other_sums = reinterpret_cast<float2*>(other + 128 * (D / 4));
+            if (sub == 1) {
+                // the products are done with the tiles that this goes over
+                if (ok) ok = mbar_wait(&o_full[0], 0, 0x7E);
+                if (ok) {
+#pragma unroll 1
+                    for (int c = 0; c < D / 16; ++c) {
+                        uint32_t ov[16];
+                        tmem_ld_x16(o_at + 16u * c, ov);
+                        tmem_ld_wait(ov);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            other[(4 * c + e) * 128 + r_sub] = make_float4(__uint_as_float(ov[4 * e]), __uint_as_float(ov[4 * e + 1]),
+                                                                           __uint_as_float(ov[4 * e + 2]), __uint_as_float(ov[4 * e + 3]));
+                    }
+                    other_sums[r_sub] = make_float2(ref, l);
+                }
+            }
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            if (sub == 0) {
+                const float2 o = other_sums[r_sub];
+                const float top = fmaxf(ref, o.x);
+                f_own = ref > -INFINITY ? exp2f(ref - top) : 0.f;
+                f_other = o.x > -INFINITY ? exp2f(o.x - top) : 0.f;
+                ref = top;
+                l = l * f_own + o.y * f_other;
+            }
+        }
+        if (ok && (sub == 0 || !alternate)) {
             const bool live = row < rows;
             const float inv = bad ? NAN : ref > -INFINITY ? vmax / l : 0.f;  // no reference: nothing was seen
             const int64_t at = p.splits > 1 ? out_row * p.splits + blockIdx.y : 0;
 #pragma unroll 2
             for (int c = 0; c < D / 16; ++c) {
                 uint32_t ov[16];
-                if (tiles > 0) {
+                if (has_o) {
                     tmem_ld_x16(o_at + 16u * c, ov);
                     tmem_ld_wait(ov);
+                    if (alternate && tiles > 1) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const float y = reinterpret_cast<const float*>(other + (4 * c + e / 4) * 128 + r_sub)[e & 3];
+                            ov[e] = __float_as_uint(fmaf(__uint_as_float(ov[e]), f_own, y * f_other));
+                        }
+                    }
                 } else {
 #pragma unroll
                     for (int e = 0; e < 16; ++e) ov[e] = 0;
@@ -479,35 +529,53 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
             __syncwarp();
             if (lane == 0) mbar_arrive(bar);
         };
-        // halves of K, then of V, the next half's loads in flight while one is converted
-        uint4 even[kPasses], odd[kPasses];
-        if (tiles > 0) {
-            ok = mbar_wait(&m_full[0], 0, 0x74);
-            if (ok) load(p.c.k_codes, 0, 0, even);
+        // Halves of K, then of V; a half's registers take the next tile's codes when they are converted, so that
+        // a whole tile's are in flight or waiting. One subtile of rows waits for the codes: it asks as early
+        // as it can. Two wait for their softmax: the loads stand behind the fence that publishes a tile, which
+        // would wait for them (prompt of 8192: 668 us, 681 with the early loads; 20 rows: 470 and 440).
+        uint4 k0[kPasses], k1[kPasses], v0[kPasses], v1[kPasses];
+        auto next = [&](const uint8_t* codes, int i, int part, uint4 (&raw)[kPasses]) {
+            if (i < tiles) load(codes, i, part, raw);
+        };
+        auto looked_up = [&](int i) {  // tile i's places have been read
+            __syncwarp();
+            if (lane == 0 && i < tiles) mbar_arrive(&m_empty[i & (kMeta - 1)]);
+        };
+        if (tiles > 0) ok = mbar_wait(&m_full[0], 0, 0x74);
+        if (ok) {
+            next(p.c.k_codes, 0, 0, k0);
+            next(p.c.k_codes, 0, 1, k1);
+            next(p.c.v_codes, 0, 0, v0);
+            next(p.c.v_codes, 0, 1, v1);
+            looked_up(0);
         }
         for (int i = 0; ok && i < tiles; ++i) {
             const int ks = 2 * (i & 1), vs = ks + 1;
             const uint32_t free_parity = ((i >> 1) & 1) ^ 1;
-            load(p.c.k_codes, i, 1, odd);
             ok = mbar_wait(&empty[ks], free_parity, 0x75);
+            if (ok && i + 1 < tiles) ok = mbar_wait(&m_full[(i + 1) & (kMeta - 1)], ((i + 1) / kMeta) & 1, 0x7B);
             if (!ok) break;
-            convert(even, ring + ks * L::kSub, 0);
-            load(p.c.v_codes, i, 0, even);
-            convert(odd, ring + ks * L::kSub, 1);
+            convert(k0, ring + ks * L::kSub, 0);
+            if (alternate) next(p.c.k_codes, i + 1, 0, k0);
+            convert(k1, ring + ks * L::kSub, 1);
+            if (alternate) next(p.c.k_codes, i + 1, 1, k1);
             done(&full[ks]);
-            load(p.c.v_codes, i, 1, odd);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&m_empty[i & (kMeta - 1)]);
+            if (!alternate) {
+                next(p.c.k_codes, i + 1, 0, k0);
+                next(p.c.k_codes, i + 1, 1, k1);
+            }
             ok = mbar_wait(&empty[vs], free_parity, 0x7C);
             if (!ok) break;
-            convert(even, ring + vs * L::kSub, 0);
-            if (i + 1 < tiles) {
-                ok = mbar_wait(&m_full[(i + 1) & (kMeta - 1)], ((i + 1) / kMeta) & 1, 0x7B);
-                if (!ok) break;
-                load(p.c.k_codes, i + 1, 0, even);
-            }
-            convert(odd, ring + vs * L::kSub, 1);
+            convert(v0, ring + vs * L::kSub, 0);
+            if (alternate) next(p.c.v_codes, i + 1, 0, v0);
+            convert(v1, ring + vs * L::kSub, 1);
+            if (alternate) next(p.c.v_codes, i + 1, 1, v1);
             done(&full[vs]);
+            if (!alternate) {
+                next(p.c.v_codes, i + 1, 0, v0);
+                next(p.c.v_codes, i + 1, 1, v1);
+            }
+            looked_up(i + 1);
         }
     } else {
       if (warp == kLookupWarp) {
@@ -528,6 +596,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
                     t.ks = __ldg(p.c.k_scales + ph);
                     t.lg = vs > 0.f ? fmaxf(log2f(vs) - lg_max, kLgMin) : kLgMin;
                     t.inv = exp2f(-t.lg);
+                    prefetch_l2(p.c.k_codes + at, 16 * D);
+                    prefetch_l2(p.c.v_codes + at, 16 * D);
                 }
             }
             for (int n = i0; ok && n < i0 + kMetaBatch && n < tiles; ++n)
@@ -558,40 +628,72 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
                     mma_ss(d, a + off, b + off, idesc_s, k > 0);
                 }
             };
-            auto pv = [&](int sub, int i) {
+            auto pv = [&](int sub, int i, bool add) {
                 const uint64_t b = v_desc + (i & 1 ? 2 * kSubUnits : 0);
                 const uint32_t d = tmem + 256 + sub * D, a = tmem + sub * 128;
 #pragma unroll 2
-                for (int k = 0; k < kTile / 16; ++k) mma_ts(d, a + 8 * k, b + k * 128, idesc_o, i > 0 || k > 0);
+                for (int k = 0; k < kTile / 16; ++k) mma_ts(d, a + 8 * k, b + k * 128, idesc_o, add || k > 0);
             };
-            ok = mbar_wait(&full[0], 0, 0x76);
-            for (int sub = 0; ok && sub < 2; ++sub) {
-                ok = mbar_wait(&q_full[sub], 0, 0x77);
-                if (!ok) break;
-                tc::tc_fence_after();
-                qk(sub, 0);
-                commit_elected(&s_full[sub]);
-            }
-            if (ok) commit_elected(&empty[0]);
-            for (int i = 0; ok && i < tiles; ++i) {
-                const uint32_t ph = (i >> 1) & 1, phn = ((i + 1) >> 1) & 1;
-                const int ks = 2 * ((i + 1) & 1), vs = 2 * (i & 1) + 1;
-                for (int sub = 0; ok && sub < 2; ++sub) {
-                    ok = mbar_wait(&p_full[sub], i & 1, 0x78) && (sub || mbar_wait(&full[vs], ph, 0x79));
+            // the first products, then each softmax group's next as its weights arrive. K's and V's tiles are in
+            // slots by their number's parity, freed when every group that reads them has its products.
+            if (alternate) {
+                for (int i = 0; ok && i < 2 && i < tiles; ++i) {
+                    ok = mbar_wait(&full[2 * i], 0, 0x76) && mbar_wait(&q_full[i], 0, 0x77);
                     if (!ok) break;
                     tc::tc_fence_after();
-                    pv(sub, i);
-                    if (i + 1 == tiles) commit_elected(&o_full[sub]);
-                    if (sub) commit_elected(&empty[vs]);
-                    if (i + 1 < tiles) {
-                        if (!sub) {
-                            ok = mbar_wait(&full[ks], phn, 0x7A);
-                            if (!ok) break;
-                            tc::tc_fence_after();
+                    qk(i, i);
+                    commit_elected(&s_full[i]);
+                    commit_elected(&empty[2 * i]);
+                }
+                for (int i = 0; ok && i < tiles; ++i) {
+                    const int sub = i & 1, ks = 2 * sub, vs = ks + 1;
+                    const uint32_t ph = (i >> 1) & 1;
+                    ok = mbar_wait(&p_full[sub], ph, 0x78) && mbar_wait(&full[vs], ph, 0x79);
+                    if (!ok) break;
+                    tc::tc_fence_after();
+                    pv(sub, i, i > 1);
+                    commit_elected(&empty[vs]);
+                    if (i + 2 >= tiles) {
+                        commit_elected(&o_full[sub]);
+                        continue;
+                    }
+                    ok = mbar_wait(&full[ks], ph ^ 1, 0x7A);
+                    if (!ok) break;
+                    tc::tc_fence_after();
+                    qk(sub, i);
+                    commit_elected(&s_full[sub]);
+                    commit_elected(&empty[ks]);
+                }
+            } else {
+                ok = mbar_wait(&full[0], 0, 0x76);
+                for (int sub = 0; ok && sub < 2; ++sub) {
+                    ok = mbar_wait(&q_full[sub], 0, 0x77);
+                    if (!ok) break;
+                    tc::tc_fence_after();
+                    qk(sub, 0);
+                    commit_elected(&s_full[sub]);
+                }
+                if (ok) commit_elected(&empty[0]);
+                for (int i = 0; ok && i < tiles; ++i) {
+                    const uint32_t ph = (i >> 1) & 1, phn = ((i + 1) >> 1) & 1;
+                    const int ks = 2 * ((i + 1) & 1), vs = 2 * (i & 1) + 1;
+                    for (int sub = 0; ok && sub < 2; ++sub) {
+                        ok = mbar_wait(&p_full[sub], i & 1, 0x78) && (sub || mbar_wait(&full[vs], ph, 0x79));
+                        if (!ok) break;
+                        tc::tc_fence_after();
+                        pv(sub, i, i > 0);
+                        if (i + 1 == tiles) commit_elected(&o_full[sub]);
+                        if (sub) commit_elected(&empty[vs]);
+                        if (i + 1 < tiles) {
+                            if (!sub) {
+                                ok = mbar_wait(&full[ks], phn, 0x7A);
+                                if (!ok) break;
+                                tc::tc_fence_after();
+                            }
+                            qk(sub, i + 1);
+                            commit_elected(&s_full[sub]);
+                            if (sub) commit_elected(&empty[ks]);
                         }
-                        qk(sub, i + 1);
-                        commit_elected(&s_full[sub]);
-                        if (sub) commit_elected(&empty[ks]);
                     }
                 }
             }

@@ -384,3 +384,22 @@ def test_a_given_stream_owns_the_memory_of_its_call(news):
     back = nvq.nv_kv_dequantize(*dev[1:], rows=step.rows, stream=side.cuda_stream)
     side.synchronize()
     assert ids.shape == (64, 2) and torch.equal(back[0], nvq.nv_kv_dequantize(*dev[1:], rows=step.rows)[0])
+
+
+ONE_SUBTILE = [  # lens, news, block, H, G: items of at most 128 rows, with tokens for 0, 1, 2 and many tiles
+    ([40, 128, 129, 300], [17, 20, 33, 64], 16, 2, 1),
+    ([1000, 257, 5000], [5, 9, 16], 64, 2, 8),
+    ([700, 2000], [40, 75], 128, 1, 7),  # 280 and 525 rows: a last tile of 24 and 13
+    ([6000], [128], 32, 1, 1),
+]
+
+
+@pytest.mark.parametrize("dtype,D,mode", [(BF16, 128, "int8"), (BF16, 64, "e4m3"), (BF16, 128, "e4m3"), (BF16, 64, "int8")])
+@pytest.mark.parametrize("case", range(len(ONE_SUBTILE)))
+def test_items_of_one_subtile(case, dtype, D, mode):
+    lens, news, block, H, G = ONE_SUBTILE[case]
+    step = R.Step(lens, news, block, seed=case, lead=1, behind=2)
+    _check(step, H, G, D, mode, dtype, 700 + case)
+    _check(step, H, G, D, mode, dtype, 720 + case, causal=False)
+    _check(step, H, G, D, mode, dtype, 740 + case, window=130)
+    _check(step, H, G, D, mode, dtype, 760 + case, q_scale=30.0, max_q=0)
