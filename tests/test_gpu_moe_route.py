@@ -219,3 +219,21 @@ def test_feeds_the_routed_block():
     assert (ids.cpu().numpy() == want).all()
     yr, a = O.moe_swiglu(x, gate, up, down, ids.cpu().long(), rw.cpu(), 64, 4)
     assert bool(O.within_tolerance(y.cpu(), yr, a, BF16).all())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,topk_groups,group_top", [
+    (15, 3, 2, 1), (160, 8, 3, 2), (66, 11, 4, 2), (96, 32, 9, 1), (33, 33, 5, 1), (372, 3, 1, 2), (21, 7, 7, 2), (1023, 3, 2, 1)])
+def test_groups_of_odd_sizes_to_the_last_expert(E, groups, topk_groups, group_top, score, dtype):
+    """Every expert of the open groups is chosen (or 64 of them), masked ones last: none that does not exist."""
+    topk = min(64, topk_groups * (E // groups))
+    bias = 0.1 * torch.randn(E, generator=torch.Generator().manual_seed(E))
+    z = _logits(50, E, dtype, E + 2)
+    z[10:20, ::3] = -float("inf")
+    z[20:30, : E // 2] = torch.finfo(torch.bfloat16).min
+    z[30:35] = -float("inf")
+    z[35:40] = 0.25  # ties everywhere
+    for b in (None, bias):
+        ids, _ = _check(z, topk, score, b, groups, topk_groups, group_top)
+        assert bool((ids.sort(1).values.diff(dim=1) > 0).all())
