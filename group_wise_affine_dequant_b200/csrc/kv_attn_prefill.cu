@@ -28,12 +28,12 @@
 // A row's reference follows its running maximum only when that passes it by
 // kSlack, so rescaling O in TMEM is rare and the softmax warps do it themselves.
 //
-// Bound: neither the tensor core (about 45 % busy) nor the exponential unit, but the chain of
+// Bound: neither the tensor core (38 % busy) nor the exponential unit (39 %), but the chain of
 // one subtile's step, about 4600 cycles for a pair of tiles: the products of both subtiles in
 // turn (1650), then a softmax of 2900, whose 128 exponentials a thread issue one in 8 cycles
 // at best (1024 of them) and in 12.7 as one warp a scheduler reaches. Measured at a prompt
-// of 8192 (32 heads over 8, D = 128), each slower than the 667 us of this form: scores held in registers through an unrolled
-// loop, four softmax warpgroups with two threads a row (745), an issuing warp a
+// of 8192 (32 heads over 8, D = 128), each slower than the 668 us (823 TFLOP/s) of this
+// form: scores held in registers through an unrolled loop, four softmax warpgroups with two threads a row (745), an issuing warp a
 // subtile, a share of the exponentials as polynomials on the FMA pipe.
 #include <cstdint>
 

@@ -12,8 +12,8 @@
 // once; a pass takes the largest head of all lanes (one warp reduction) and moves
 // that lane's keys up. Bound by the logits' read for many tokens (the sort and the
 // passes take about as many issue slots) and by latency for few: 16384 tokens of 256 experts,
-// 8 groups, with a bias take 31 us (the logits' read 2.7; about 1100 instructions a token, of which a
-// warp issues one in 2 cycles, and 8 us of fp64 ranking); one token 4.5 us a call. Groups
+// 8 groups, with a bias take 31 us (the logits' read 2.7; about 1200 instructions a token, at which
+// the schedulers issue 78 % of the time, and 8 us of fp64 ranking); one token 4.5 us a call. Groups
 // that are not whole runs of lanes used to be left to the fp64 ranking: 160 experts in 8 groups 94 us, now 15.
 //
 // Who is chosen is exact: scores that differ only beyond fp32, or in the bits that a
