@@ -646,14 +646,14 @@ kv_attn_decode_kernel(const __grid_constant__ DecodeArgs p, const __grid_constan
 
 // Join the chunks of the rows whose sequence took several: one CTA per row of
 // partials, of one warp per eight chunks there can be; warp w sums chunks w, w + warps,
-// ... in order (its loads all in flight), then the warps' sums are added in order.
-constexpr int kJoinWarps = 16;
+// ... in order (eight's loads in flight), then the warps' sums are added in order.
+// The row's sequence is found while the kernel before still runs: what wrote the descriptor
+// had ended when that one began (1 x 4096: 16.8 -> 14.7 us, 2 x 131072: 104 -> 98).
+constexpr int kJoinWarps = 16, kJoinAhead = 8;
 template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) kv_attn_join_kernel(const __grid_constant__ DecodeArgs p) {
     __shared__ float sums[kJoinWarps][D];
     __shared__ float weights[kJoinWarps];
-    pdl_launch_dependents();
-    pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int G = p.a.Hq / p.c.H;
     int64_t t;
@@ -670,25 +670,43 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv_attn_join_kernel(const __g
         s = kv_find_seq(p.st, t, 1, 1, 0);
     }
     const SeqWork w = seq_work(p, s);
+    pdl_launch_dependents();
+    pdl_wait();
     if (t < w.span.row0 || t >= w.span.row0 + w.span.n || w.tiles == 0 || w.chunks <= 1) return;
     const int64_t at = static_cast<int64_t>(blockIdx.x) * p.max_chunks;
+    constexpr int V = D / 32;  // values a lane
+    float2 x[kJoinAhead][V / 2];
+    float lse[kJoinAhead];
+    auto load = [&](int k0) {
+#pragma unroll
+        for (int j = 0; j < kJoinAhead; ++j) {
+            const int k = k0 + j * warps;
+            lse[j] = k < w.chunks ? __ldcg(p.part_lse + at + k) : -INFINITY;
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i)
+                x[j][i] = k < w.chunks ? __ldcg(reinterpret_cast<const float2*>(p.part_o + (at + k) * D + lane * V) + i)
+                                       : make_float2(0.f, 0.f);
+        }
+    };
+    load(warp);
     float top = -INFINITY;
     for (int k = lane; k < w.chunks; k += 32) top = fmaxf(top, __ldcg(p.part_lse + at + k));
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     if (top == -INFINITY) top = 0.f;
-    constexpr int V = D / 32;  // values a lane
     float acc[V] = {};
     float weight = 0.f;
-#pragma unroll 8
-    for (int k = warp; k < w.chunks; k += warps) {
-        const float e = exp2f(__ldcg(p.part_lse + at + k) - top);
-        weight += e;
+    for (int k0 = warp; k0 < w.chunks; k0 += kJoinAhead * warps) {
+        if (k0 > warp) load(k0);
 #pragma unroll
-        for (int i = 0; i < V; i += 2) {
-            const float2 x = __ldcg(reinterpret_cast<const float2*>(p.part_o + (at + k) * D + lane * V + i));
-            acc[i] = fmaf(e, x.x, acc[i]);
-            acc[i + 1] = fmaf(e, x.y, acc[i + 1]);
+        for (int j = 0; j < kJoinAhead; ++j) {
+            const float e = exp2f(lse[j] - top);
+            weight += e;
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) {
+                acc[2 * i] = fmaf(e, x[j][i].x, acc[2 * i]);
+                acc[2 * i + 1] = fmaf(e, x[j][i].y, acc[2 * i + 1]);
+            }
         }
     }
 #pragma unroll
