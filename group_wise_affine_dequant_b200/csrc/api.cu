@@ -439,13 +439,16 @@ nv_status nv_kv_attention(const void* q, int64_t q_stride, nv_dtype dt, int64_t 
     const int sms = sm_count();
     const KvAttnPlan plan = kv_attn_plan(dt, rows, Hq, H, block, D, max_pages, S, max_q, sms);
     if (P > 0 && (plan.decode || plan.prefill)) {
-        if (plan.decode) {
-            st = from_cuda(nvq::launch_kv_attn_decode(a, c, steps, plan.d, workspace, stream, sms));
-            if (st != NV_OK) return st;
-        }
-        if (!plan.prefill) return NV_OK;
-        return from_cuda(nvq::launch_kv_attn_prefill(a, c, steps, plan.p, plan.decode ? plan.d.row_limit : 0,
-                                                     static_cast<char*>(workspace) + plan.decode_bytes, stream));
+        // Of the two kernels the one for many rows goes first: the other, whose CTAs are small, begins
+        // on the SMs that it leaves free.
+        void* parts = static_cast<char*>(workspace) + plan.decode_bytes;
+        const int row_min = plan.decode ? plan.d.row_limit : 0;
+        if (plan.prefill) st = from_cuda(nvq::launch_kv_attn_prefill(a, c, steps, plan.p, row_min, parts, stream));
+        if (st == NV_OK && plan.decode)
+            st = from_cuda(nvq::launch_kv_attn_decode(a, c, steps, plan.d, workspace, plan.prefill, stream, sms));
+        if (st == NV_OK && plan.prefill)
+            st = from_cuda(nvq::launch_kv_attn_prefill_join(a, c, steps, plan.p, row_min, parts, stream));
+        return st;
     }
     return from_cuda(nvq::launch_kv_attn_simple(a, c, steps, stream));
 }

@@ -146,7 +146,8 @@ cudaError_t launch_kv_attn_simple(const KvAttn& a, const KvCache& c, const KvSte
 
 // Kernel for few rows a sequence (bf16, D 64 or 128): sequences are cut into
 // chunks that a second kernel joins. `only`: every sequence is its; else it takes those of at
-// most 16 flattened rows (token, head of the group) and leaves the others.
+// most 16 flattened rows (token, head of the group) and leaves the others. `beside`: it is launched behind the
+// kernel for many rows, nothing of whose it reads, and begins when that one's last CTAs have.
 struct KvDecodeSizes {
     int64_t rows, S, max_pages;
     int Hq, H, block, D;
@@ -167,11 +168,11 @@ struct KvDecodePlan {
 };
 KvDecodePlan kv_decode_plan(const KvDecodeSizes& z, int num_sms);
 cudaError_t launch_kv_attn_decode(const KvAttn& a, const KvCache& c, const KvSteps& st, const KvDecodePlan& plan,
-                                  void* workspace, cudaStream_t stream, int num_sms);
+                                  void* workspace, bool beside, cudaStream_t stream, int num_sms);
 unsigned int kv_attn_decode_error_take();
 
 // Tensor-core kernel for many rows a sequence (bf16, D 64 or 128); sequences of at
-// most row_min flattened rows are left to the other.
+// most row_min flattened rows are left to the other. A second launch joins the parts that tokens were cut into.
 struct KvPrefillSizes {
     int64_t rows, S, max_pages;
     int Hq, H, block, D;
@@ -184,6 +185,8 @@ struct KvPrefillPlan {
 KvPrefillPlan kv_prefill_plan(const KvPrefillSizes& z, int num_sms);
 cudaError_t launch_kv_attn_prefill(const KvAttn& a, const KvCache& c, const KvSteps& st, const KvPrefillPlan& plan,
                                    int row_min, void* workspace, cudaStream_t stream);
+cudaError_t launch_kv_attn_prefill_join(const KvAttn& a, const KvCache& c, const KvSteps& st, const KvPrefillPlan& plan,
+                                        int row_min, void* workspace, cudaStream_t stream);
 unsigned int kv_attn_prefill_error_take();
 
 }  // namespace nvq

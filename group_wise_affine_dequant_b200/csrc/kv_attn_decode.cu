@@ -78,6 +78,7 @@ struct DecodeArgs {
     int tile_rows;   // 8 or 16
     int lg_block;    // log2 of the cache's block
     int row_limit;   // sequences of more flattened rows are not this kernel's (0: all are)
+    bool beside;     // launched on the kernel for many rows, beside whose end it runs
     float* part_o;   // [rows][max_chunks][D]
     float* part_lse; // [rows][max_chunks]
 };
@@ -151,7 +152,7 @@ kv_attn_decode_kernel(const __grid_constant__ DecodeArgs p, const __grid_constan
         mbar_init_fence();
     }
     pdl_launch_dependents();
-    pdl_wait();
+    if (!p.beside) pdl_wait();
 
     // items before each thread's run of sequences
     const int G = p.a.Hq / p.c.H;
@@ -642,6 +643,8 @@ kv_attn_decode_kernel(const __grid_constant__ DecodeArgs p, const __grid_constan
             if (lane == 0) mbar_arrive(&meta_empty[slot]);
         }
     }
+    // what follows waits for this kernel, so this one for the kernel that it ran beside
+    if (p.beside) pdl_wait();
 }
 
 // Join the chunks of the rows whose sequence took several: one CTA per row of
@@ -744,7 +747,8 @@ cudaError_t launch(const DecodeArgs& p, int64_t part_rows, cudaStream_t stream, 
     constexpr int smem = 1024 + kStages<D> * 2 * kTile * D + 8 * NQ * D * 4;
     cudaError_t e = cudaFuncSetAttribute(kv_attn_decode_kernel<MODE, D, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    // Not launched programmatically: its items are dealt out for one wave of CTAs, and those that
+    // Not launched programmatically, but for the call's own kernel for many rows (512 new tokens of one sequence
+    // and single ones of 31, 8192 long: 297 -> 278 us): its items are dealt out for one wave of CTAs, and those that
     // start beside the previous kernel's last ones do so unevenly (64 x 8192: 214 us so, 146 us not).
     cudaLaunchAttribute pdl[1];
     pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -757,9 +761,10 @@ cudaError_t launch(const DecodeArgs& p, int64_t part_rows, cudaStream_t stream, 
     cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
+    cfg.attrs = pdl;
+    cfg.numAttrs = p.beside ? 1 : 0;
     e = cudaLaunchKernelEx(&cfg, kv_attn_decode_kernel<MODE, D, NQ>, p, kmap, vmap);
     if (e != cudaSuccess || p.max_chunks <= 1) return e;
-    cfg.attrs = pdl;
     cfg.numAttrs = 1;
     cfg.gridDim = dim3(static_cast<unsigned>(part_rows), 1, 1);
     const int warps = (p.max_chunks + 7) / 8;
@@ -793,9 +798,10 @@ KvDecodePlan kv_decode_plan(const KvDecodeSizes& z, int num_sms) {
 }
 
 cudaError_t launch_kv_attn_decode(const KvAttn& a, const KvCache& c, const KvSteps& st, const KvDecodePlan& plan,
-                                  void* workspace, cudaStream_t stream, int num_sms) {
+                                  void* workspace, bool beside, cudaStream_t stream, int num_sms) {
     const int lg_block = c.block == 16 ? 4 : c.block == 32 ? 5 : c.block == 64 ? 6 : 7;
-    DecodeArgs p{a, c, st, plan.target, kChunkMax, plan.max_chunks, plan.tile_rows, lg_block, plan.row_limit, nullptr, nullptr};
+    DecodeArgs p{a, c, st, plan.target, kChunkMax, plan.max_chunks, plan.tile_rows, lg_block, plan.row_limit, beside,
+                 nullptr, nullptr};
     if (plan.max_chunks > 1) {
         p.part_o = static_cast<float*>(workspace);
         p.part_lse = p.part_o + plan.part_rows * plan.max_chunks * c.D;

@@ -750,23 +750,35 @@ cudaError_t launch(const PrefillArgs& p, cudaStream_t stream) {
                                          Smem<D>::kBytes);
     if (e != cudaSuccess) return e;
     // Not launched programmatically: its CTAs take a whole SM each, and early ones only keep the last
-    // of the kernel before it from theirs (ragged chunks, behind the kernel for few rows: 335 -> 320 us).
-    cudaLaunchAttribute pdl[1];
-    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    pdl[0].val.programmaticStreamSerializationAllowed = 1;
+    // of the kernel before it from theirs (ragged chunks, behind another kernel: 335 -> 320 us).
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(p.items * p.c.H), p.splits, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.dynamicSmemBytes = Smem<D>::kBytes;
     cfg.stream = stream;
-    e = cudaLaunchKernelEx(&cfg, kv_attn_prefill_kernel<MODE, D>, p);
-    if (e != cudaSuccess || p.splits <= 1) return e;
-    cfg.attrs = pdl;
-    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kv_attn_prefill_kernel<MODE, D>, p);
+}
+template <int D>
+cudaError_t launch_join(const PrefillArgs& p, cudaStream_t stream) {
+    cudaLaunchAttribute pdl[1];
+    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    pdl[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>((p.st.rows * p.a.Hq + 3) / 4), 1, 1);
     cfg.blockDim = dim3(128, 1, 1);
-    cfg.dynamicSmemBytes = 0;
+    cfg.stream = stream;
+    cfg.attrs = pdl;
+    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kv_attn_prefill_join_kernel<D>, p);
+}
+PrefillArgs prefill_args(const KvAttn& a, const KvCache& c, const KvSteps& st, const KvPrefillPlan& plan, int row_min,
+                         void* workspace) {
+    PrefillArgs p{a, c, st, plan.items, plan.splits, row_min, nullptr, nullptr};
+    if (plan.splits > 1) {
+        p.part_o = static_cast<float*>(workspace);
+        p.part_lse = p.part_o + st.rows * a.Hq * plan.splits * c.D;
+    }
+    return p;
 }
 
 }  // namespace
@@ -787,14 +799,17 @@ KvPrefillPlan kv_prefill_plan(const KvPrefillSizes& z, int num_sms) {
 
 cudaError_t launch_kv_attn_prefill(const KvAttn& a, const KvCache& c, const KvSteps& st, const KvPrefillPlan& plan,
                                    int row_min, void* workspace, cudaStream_t stream) {
-    PrefillArgs p{a, c, st, plan.items, plan.splits, row_min, nullptr, nullptr};
-    if (plan.splits > 1) {
-        p.part_o = static_cast<float*>(workspace);
-        p.part_lse = p.part_o + st.rows * a.Hq * plan.splits * c.D;
-    }
+    const PrefillArgs p = prefill_args(a, c, st, plan, row_min, workspace);
     if (c.D == 128)
         return c.mode == NV_KV_INT8 ? launch<NV_KV_INT8, 128>(p, stream) : launch<NV_KV_E4M3, 128>(p, stream);
     return c.mode == NV_KV_INT8 ? launch<NV_KV_INT8, 64>(p, stream) : launch<NV_KV_E4M3, 64>(p, stream);
+}
+
+cudaError_t launch_kv_attn_prefill_join(const KvAttn& a, const KvCache& c, const KvSteps& st, const KvPrefillPlan& plan,
+                                        int row_min, void* workspace, cudaStream_t stream) {
+    if (plan.splits <= 1) return cudaSuccess;
+    const PrefillArgs p = prefill_args(a, c, st, plan, row_min, workspace);
+    return c.D == 128 ? launch_join<128>(p, stream) : launch_join<64>(p, stream);
 }
 
 }  // namespace nvq

@@ -403,3 +403,42 @@ def test_items_of_one_subtile(case, dtype, D, mode):
     _check(step, H, G, D, mode, dtype, 720 + case, causal=False)
     _check(step, H, G, D, mode, dtype, 740 + case, window=130)
     _check(step, H, G, D, mode, dtype, 760 + case, q_scale=30.0, max_q=0)
+
+
+@pytest.mark.parametrize("D,mode", [(128, "int8"), (64, "e4m3")])
+def test_both_kernels_in_a_row_of_calls(D, mode):
+    """Calls of many-row and single-token sequences, cut into parts that are joined, one behind the other
+    with one workspace, one cache and no gap: each gives what it gives alone."""
+    H, G, block = 1, 4, 64
+    cases = [([5000, 3000, 9000], [40, 1, 3]), ([9000, 700, 40, 4100], [1, 300, 1, 70]), ([2000, 2000], [4, 5])]
+    steps = [R.Step(lens, news, block, seed=20 + i) for i, (lens, news) in enumerate(cases)]
+    P = max(s.P for s in steps)
+    caches = (*_cache(P, H, block, D, mode, 1), *_cache(P, H, block, D, mode, 2))
+    dev = [t.cuda() for t in (caches[0].view(R.MODES[mode]), caches[1], caches[2].view(R.MODES[mode]), caches[3])]
+    calls, want, need = [], [], 0
+    for i, s in enumerate(steps):
+        q = torch.randn(s.rows, H * G, D, generator=torch.Generator().manual_seed(30 + i)).to(BF16)
+        out, *terms = R.attention(q, *caches, s, mode, D ** -0.5)
+        calls.append((q.cuda(), s.dev(), s.max_q))
+        alone = nvq.nv_kv_attention(calls[-1][0], *dev, *calls[-1][1], max_q=s.max_q)
+        torch.cuda.synchronize()
+        room = R.attention_tolerance(out, terms, BF16, D, max(s.lens))
+        assert bool(((alone.cpu().double() - out).abs() <= room).all())
+        want.append(alone)
+        need = max(need, nvq.nv_kv_attention_workspace_size(s.rows, H * G, H, block, D, s.pages.shape[1], len(s.lens), s.max_q))
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+
+    def row():
+        return [nvq.nv_kv_attention(q, *dev, *d, max_q=m, workspace=ws) for _ in range(6) for q, d, m in calls]
+
+    for got in (row(), None):
+        if got is None:
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                got = row()
+            for _ in range(3):
+                graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(g, want[i % 3]) for i, g in enumerate(got))
+    assert nvq.nv_pipeline_error() == 0
+    del graph
