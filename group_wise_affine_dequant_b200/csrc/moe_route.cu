@@ -535,14 +535,20 @@ cudaError_t launch(const RouteArgs& a, int vpl, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = pdl;
     cfg.numAttrs = 1;
-    switch (vpl) {
-        case 1: return cudaLaunchKernelEx(&cfg, moe_route_kernel<DT, 1>, a);
-        case 2: return cudaLaunchKernelEx(&cfg, moe_route_kernel<DT, 2>, a);
-        case 4: return cudaLaunchKernelEx(&cfg, moe_route_kernel<DT, 4>, a);
-        case 8: return cudaLaunchKernelEx(&cfg, moe_route_kernel<DT, 8>, a);
-        case 16: return cudaLaunchKernelEx(&cfg, moe_route_kernel<DT, 16>, a);
-        default: return cudaLaunchKernelEx(&cfg, moe_route_kernel<DT, 32>, a);
+    auto kernel = vpl == 1   ? moe_route_kernel<DT, 1>
+                  : vpl == 2 ? moe_route_kernel<DT, 2>
+                  : vpl == 4 ? moe_route_kernel<DT, 4>
+                  : vpl == 8 ? moe_route_kernel<DT, 8>
+                  : vpl == 16 ? moe_route_kernel<DT, 16>
+                              : moe_route_kernel<DT, 32>;
+    // up to 64 KB (1023 experts, each a group); beyond what every launch may ask for, with the 1 KB of s_sel beside it
+    constexpr size_t kStatic = sizeof(int) * kWarps * kMaxTopk, kFree = 48 * 1024;
+    if (cfg.dynamicSmemBytes + kStatic > kFree) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   static_cast<int>(cfg.dynamicSmemBytes));
+        if (e != cudaSuccess) return e;
     }
+    return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 }  // namespace

@@ -237,3 +237,13 @@ def test_groups_of_odd_sizes_to_the_last_expert(E, groups, topk_groups, group_to
     for b in (None, bias):
         ids, _ = _check(z, topk, score, b, groups, topk_groups, group_top)
         assert bool((ids.sort(1).values.diff(dim=1) > 0).all())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("E,groups,group_top", [(1023, 1023, 1), (1008, 504, 2), (768, 768, 2), (752, 752, 1), (753, 753, 1), (1020, 510, 1)])
+def test_hundreds_of_groups(E, groups, group_top, dtype):
+    """The ranking of many groups keeps E + groups doubles a token: more than 48 KB of shared memory a block here."""
+    bias = 0.1 * torch.randn(E, generator=torch.Generator().manual_seed(E))
+    z = _logits(9, E, dtype, E + 3)
+    for b in (None, bias):
+        _check(z, 8, "sigmoid", b, groups, 20, group_top)
