@@ -436,8 +436,8 @@ size_t nv_kv_attention_workspace_size(nv_dtype dt, int64_t rows, int Hq, int H, 
  * q       [rows, Hq, D] in `dt` (NV_F32 or NV_BF16), rows q_stride elements apart
  *         (as k_stride above); out [rows, Hq, D] dense in `dt`. Hq a multiple of H, at most 65536;
  *         rows * Hq below 2^31, S * H at most 2^27 - 1.
- *         q must be finite: a row that holds NaN or infinities gives no number
- *         and changes no other row.
+ *         q must be finite and its scores within fp32's range: a row that holds NaN or
+ *         infinities, or whose scores overflow, gives no number and changes no other row.
  * max_q   the largest number of rows of one sequence if known, else 0: a hint
  *         that chooses kernels, results do not depend on its being right.
  * workspace 16-byte aligned, nv_kv_attention_workspace_size(...) bytes; its

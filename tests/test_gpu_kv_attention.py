@@ -442,3 +442,25 @@ def test_both_kernels_in_a_row_of_calls(D, mode):
         assert all(torch.equal(g, want[i % 3]) for i, g in enumerate(got))
     assert nvq.nv_pipeline_error() == 0
     del graph
+
+
+@pytest.mark.parametrize("mode", ["int8", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("news", [1, 60])
+@pytest.mark.parametrize("size", [2.0 ** 112, 2.0 ** 116, 1e36, 3e37, 2.0 ** -112, 2.0 ** -118, 1e-36, 1e-38, 1e-39])
+def test_queries_at_the_ends_of_the_range(size, news, D, mode):
+    """Queries up to the largest bf16 and down to its subnormals, against keys that bring the scores back
+    to about 1. (Queries become fp16 times a power of two exactly here: no room is added for them.)"""
+    H, G = 1, 4
+    step = R.Step([300], [news], 64, seed=13)
+    kraw, ks = _cache(step.P, H, 64, D, mode, 1)
+    caches = (kraw, (ks.double() / size).clamp_max(1e36).float(), *_cache(step.P, H, 64, D, mode, 2))
+    q = (torch.randn(step.rows, H * G, D, generator=torch.Generator().manual_seed(3)).double() * size).to(BF16)
+    if size > 1:
+        q[0, 0, 0] = torch.finfo(BF16).max
+    for scale in (D ** -0.5, -D ** -0.5):
+        got = _run(step, q, caches, mode, scale=scale, max_q=news)
+        out, *terms = R.attention(q, *caches, step, mode, scale)
+        room = R.attention_tolerance(out, terms, BF16, D, 300)
+        err = (got.double() - out).abs()
+        assert bool((err <= room).all()), float((err / room).max())
