@@ -464,3 +464,26 @@ def test_queries_at_the_ends_of_the_range(size, news, D, mode):
         room = R.attention_tolerance(out, terms, BF16, D, 300)
         err = (got.double() - out).abs()
         assert bool((err <= room).all()), float((err / room).max())
+
+
+@pytest.mark.parametrize("mode", ["int8", "e4m3"])
+@pytest.mark.parametrize("dtype,D", [(F32, 64), (F32, 256), (BF16, 80), (BF16, 64), (BF16, 128)])
+@pytest.mark.parametrize("news", [1, 40])
+@pytest.mark.parametrize("size", [2.0 ** 114, 3e37, 2.0 ** -112, 1e-38, 1e-39])
+def test_queries_and_values_at_the_ends_of_the_range(size, news, dtype, D, mode):
+    """Every kernel: queries as above, and values up to the largest number or down to the smallest normal
+    ones, whose sum over the tokens would leave the range. Results below 1e-30 only have to be finite."""
+    H, G = 1, 2
+    step = R.Step([300], [news], 64, seed=14)
+    kraw, ks = _cache(step.P, H, 64, D, mode, 1)
+    vraw, vs = _cache(step.P, H, 64, D, mode, 2)
+    vs = vs * (3e38 / R.LARGEST[mode] / float(vs.max()) if size > 1 else 2.0 ** -110)
+    caches = (kraw, (ks.double() / size).clamp_max(1e36).float(), vraw, vs)
+    q = (torch.randn(step.rows, H * G, D, generator=torch.Generator().manual_seed(3)).double() * size).to(dtype)
+    if size > 1:
+        q[0, 0, 0] = 3.3e38
+    got = _run(step, q, caches, mode, max_q=news)
+    out, *terms = R.attention(q, *caches, step, mode, D ** -0.5)
+    room = R.attention_tolerance(out, terms, dtype, D, 300)
+    err = (got.double() - out).abs()
+    assert bool((err <= room).all()), float((err / room).max())
