@@ -19,13 +19,16 @@
 // blocks turn from accumulators to operands by movmatrix. No barrier between the
 // warps inside an item; they join at its end. Items of a sequence that
 // takes several write (output, log-sum) to the workspace and a second kernel
-// joins them in chunk order, so results do not depend on timing.
+// joins them in chunk order, so results do not depend on timing. An item whose value scales are too far apart
+// for fp16 weights (2^24) is read row by row in fp32 by the same warps (one such block in
+// each of 64 sequences of 8192: 0.14 -> 2.4 ms).
 //
 // Bound: the code bytes, 2 * D a token and key/value head. What it takes to reach
 // them is warps in flight (a warp's step is one long chain): 3 CTAs an SM.
 #include <cstdint>
 
 #include "kv_mma.cuh"
+#include "kv_plain.cuh"
 
 namespace nvq {
 namespace {
@@ -57,6 +60,7 @@ struct ItemMeta {
     int chunk, pstride; // partial index of row r: part + r * pstride (+ chunk)
     int block0;         // t0 / block
     float vmax;         // largest value scale of the item
+    bool wide;          // value scales too far apart for fp16 weights: no stages, the rows go one by one
 };
 
 // Chunk length for a span of tokens: `target` chunks a sequence where the GPU would be
@@ -115,6 +119,27 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t a) {
     uint32_t d;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
     return d;
+}
+
+// The rows of a wide item, one after the other, by the four consumer warps.
+template <int MODE, int D>
+__device__ __noinline__ void wide_item(const DecodeArgs& p, const ItemMeta& m, PlainScratch<D>& scratch) {
+    const int G = p.a.Hq / p.c.H, d = threadIdx.x;
+    const SeqSpan span{m.row0, m.len - m.first, m.len, m.first};
+    for (int row = 0; row < m.rows; ++row) {
+        const int f = m.f0 + row, hq = m.h * G + f % G;
+        const int64_t t = m.row0 + f / G;
+        const PlainRow r = plain_row<NV_BF16, MODE>(p.a, p.c, p.st, m.s, span, t, hq, m.t0, m.t1, d, scratch,
+                                                    [] { asm volatile("bar.sync 1, 128;" ::: "memory"); });
+        if (m.part < 0) {
+            if (d < D) static_cast<uint16_t*>(p.a.out)[(t * p.a.Hq + hq) * D + d] = f32_to_bf16_bits(r.out[0]);
+        } else {
+            const int64_t at = part_row(p, span, m.s, m.h, f) * p.max_chunks + m.chunk;
+            if (d < D) p.part_o[at * D + d] = r.out[0];
+            // the other items' sums carry 2^kLift, and count no row that is not a number
+            if (d == 0) p.part_lse[at] = r.l != r.l ? 0.f : r.l > 0.f ? r.m * kLog2e + log2f(r.l) + kLift : -INFINITY;
+        }
+    }
 }
 
 // NQ: groups of 8 query rows a tile.
@@ -267,15 +292,18 @@ kv_attn_decode_kernel(const __grid_constant__ DecodeArgs p, const __grid_constan
             }
 #pragma unroll
             for (int o = 16; o; o >>= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, o));
+            bool wide = false;
 #pragma unroll
             for (int i = 0; i < (kBlocksMax + 31) / 32; ++i) {
                 const int b = lane + 32 * i;
                 if (b < blocks) {
-                    const float lg = vs_of[i] > 0.f ? fmaxf(log2f(vs_of[i]) - log2f(vmax), kLgMin) : kLgMin;
+                    const float lg = vs_of[i] > 0.f ? log2f(vs_of[i]) - log2f(vmax) : kLgZero;
+                    wide |= vs_of[i] > 0.f && lg < kLgWide;
                     scales[slot][b].lg = lg;
                     scales[slot][b].inv = exp2f(-lg);
                 }
             }
+            wide = __any_sync(0xffffffffu, wide);
             if (lane == 0) {
                 ItemMeta& m = meta[slot];
                 m.row0 = sw.span.row0;
@@ -293,6 +321,7 @@ kv_attn_decode_kernel(const __grid_constant__ DecodeArgs p, const __grid_constan
                 m.chunk = chunk;
                 m.block0 = block0;
                 m.vmax = vmax;
+                m.wide = wide;
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&meta_full[slot]);
@@ -300,7 +329,8 @@ kv_attn_decode_kernel(const __grid_constant__ DecodeArgs p, const __grid_constan
         if (blockIdx.x < total) prepare(blockIdx.x, 0);
         int it = 0;
         for (int64_t w = blockIdx.x; ok && w < total; w += gridDim.x, ++it) {
-            const int slot = it & 1, t0 = meta[slot].t0, t1 = meta[slot].t1, block0 = meta[slot].block0, h = meta[slot].h;
+            const int slot = it & 1, t0 = meta[slot].t0, t1 = meta[slot].wide ? t0 : meta[slot].t1;
+            const int block0 = meta[slot].block0, h = meta[slot].h;
             for (int t = t0; ok && t < t1; t += kTile) {
                 ok = mbar_wait(&empty[stage], phase ^ 1, 0x62);
                 if (!ok) break;
@@ -351,6 +381,13 @@ kv_attn_decode_kernel(const __grid_constant__ DecodeArgs p, const __grid_constan
             asm volatile("bar.sync 1, 128;" ::: "memory");
             if (failed) break;
             const ItemMeta& m = meta[slot];
+            if (m.wide) {
+                static_assert(sizeof(PlainScratch<D>) <= RT * D * sizeof(float), "");
+                wide_item<MODE, D>(p, m, *reinterpret_cast<PlainScratch<D>*>(join));
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+                if (lane == 0) mbar_arrive(&meta_empty[slot]);
+                continue;
+            }
             // queries as B operands: lane 4 g + t4 holds values t4 * D / 4 .. of row g (of each group of 8)
             uint32_t qb[NQ][KS][2];
             float zc[NQ][2];               // of the lane's two score columns, rows 2 t4 and 2 t4 + 1

@@ -25,6 +25,8 @@
 //
 // Block scales never touch the tiles: keys' are factors of the scores, values' join
 // the exponent (weights are 2^(z + lg)), and the weights' sum takes them out again.
+// An item whose value scales are too far apart for that (2^24; blocks of zeros do not count) goes row by
+// row in fp32: a prompt of 8192 with one such block takes 70 ms if it is the last, 250 if the first.
 // A row's reference follows its running maximum only when that passes it by
 // kSlack, so rescaling O in TMEM is rare and the softmax warps do it themselves.
 //
@@ -38,6 +40,7 @@
 #include <cstdint>
 
 #include "kv_mma.cuh"
+#include "kv_plain.cuh"
 
 namespace nvq {
 namespace {
@@ -146,6 +149,28 @@ __device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
 // queries are all zero, so that a score of -infinity (not seen) stays one.
 __device__ __forceinline__ float score_factor(float zc, float ks) { return fmaxf(zc * ks, 1e-37f); }
 
+// The rows of a wide item (value scales too far apart for fp16 weights), every fourth by each 128 threads.
+template <int MODE, int D>
+__device__ __noinline__ void wide_item(const PrefillArgs& p, const SeqSpan span, int s, int h, int f0, int rows, int lo, int hi,
+                                       PlainScratch<D>* scratch) {
+    constexpr int kTeams = kThreads / kPlainThreads;
+    const int G = p.a.Hq / p.c.H, team = threadIdx.x / kPlainThreads, d = threadIdx.x % kPlainThreads;
+    for (int row = team; row < rows; row += kTeams) {
+        const int f = f0 + row, hq = h * G + f % G;
+        const int64_t t = span.row0 + f / G, at = t * p.a.Hq + hq;
+        const PlainRow r = plain_row<NV_BF16, MODE>(p.a, p.c, p.st, s, span, t, hq, lo, hi, d, scratch[team], [team] {
+            asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(kPlainThreads) : "memory");
+        });
+        if (p.splits > 1) {
+            const int64_t part = at * p.splits + blockIdx.y;
+            if (d < D) p.part_o[part * D + d] = r.out[0];
+            if (d == 0) p.part_lse[part] = r.l != r.l ? 0.f : r.l > 0.f ? r.m * kLog2e + log2f(r.l) : -INFINITY;
+        } else if (d < D) {
+            static_cast<uint16_t*>(p.a.out)[at * D + d] = f32_to_bf16_bits(r.out[0]);
+        }
+    }
+}
+
 template <int D>
 struct Smem {
     static constexpr int kHalves = D / 64;
@@ -166,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
         m_full[kMeta], m_empty[kMeta];
     __shared__ ChunkScales scales[kMeta][kChunks];
     __shared__ int64_t places[kMeta][kChunks];  // byte offset of the chunk's codes of this head, -1: none
-    __shared__ uint32_t tmem_slot, vmax_bits;
+    __shared__ uint32_t tmem_slot, vmax_bits, vmin_bits;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
     pdl_launch_dependents();
@@ -203,6 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
         }
         mbar_init_fence();
         vmax_bits = 0;
+        vmin_bits = 0x7F800000u;
     }
     int lo = 0, hi = span.len;
     if (p.a.causal) {
@@ -222,17 +248,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
         if (lo + tiles * kTile < hi) hi = lo + tiles * kTile;
     }
 
-    // ---- the largest value scale of the item: weights carry value scales relative to it
+    // ---- the largest value scale of the item: weights carry value scales relative to it (and the smallest but zero)
     if (tiles > 0) {
         const int b0 = (lo > lo_seen ? lo : lo_seen) / p.c.block, b1 = (hi - 1) / p.c.block;
-        float most = 0.f;
+        float most = 0.f, least = INFINITY;
         for (int b = b0 + tid; b <= b1; b += kThreads) {
             const int32_t page = __ldg(p.st.pages + static_cast<int64_t>(s) * p.st.max_pages + b);
-            if (page >= 0 && page < p.c.P) most = fmaxf(most, __ldg(p.c.v_scales + static_cast<int64_t>(page) * p.c.H + h));
+            if (page >= 0 && page < p.c.P) {
+                const float vs = __ldg(p.c.v_scales + static_cast<int64_t>(page) * p.c.H + h);
+                most = fmaxf(most, vs);
+                if (vs > 0.f) least = fminf(least, vs);
+            }
         }
-        __syncthreads();  // vmax_bits initialised
+        __syncthreads();  // vmax_bits and vmin_bits initialised
         const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(most));
-        if (lane == 0 && bits) atomicMax(&vmax_bits, bits);
+        const uint32_t low_bits = __reduce_min_sync(0xffffffffu, __float_as_uint(least));
+        if (lane == 0 && bits) {
+            atomicMax(&vmax_bits, bits);
+            atomicMin(&vmin_bits, low_bits);
+        }
     }
     if (warp == kIssueWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)),
@@ -246,7 +280,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
     const float vmax = __uint_as_float(vmax_bits);
     bool ok = true;
 
-    if (warp >= kSoftmaxWarp0 && warp < kSoftmaxWarp0 + kSoftmaxWarps) {
+    if (vmax > 0.f && log2f(__uint_as_float(vmin_bits)) - log2f(vmax) < kLgWide) {
+        wide_item<MODE, D>(p, span, s, h, f0, rows, lo, hi, reinterpret_cast<PlainScratch<D>*>(q_smem));
+    } else if (warp >= kSoftmaxWarp0 && warp < kSoftmaxWarp0 + kSoftmaxWarps) {
         // ------------------------------------------------------------- softmax
         const int sub = (warp - kSoftmaxWarp0) >> 2;
         const int r_sub = tid & 127;              // row of the subtile = TMEM lane
@@ -594,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_prefill_kernel(const __gr
                     const float vs = __ldg(p.c.v_scales + ph);
                     at = (ph * p.c.block + (j - b * p.c.block)) * D;
                     t.ks = __ldg(p.c.k_scales + ph);
-                    t.lg = vs > 0.f ? fmaxf(log2f(vs) - lg_max, kLgMin) : kLgMin;
+                    t.lg = vs > 0.f ? log2f(vs) - lg_max : kLgZero;
                     t.inv = exp2f(-t.lg);
                     prefetch_l2(p.c.k_codes + at, 16 * D);
                     prefetch_l2(p.c.v_codes + at, 16 * D);

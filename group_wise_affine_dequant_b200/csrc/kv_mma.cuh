@@ -69,16 +69,19 @@ __device__ __forceinline__ float pow2_bits(uint32_t biased) { return __uint_as_f
 // scale over the item's largest, M a reference that the running maximum of
 // z + lg may pass by kSlack before the sums are rescaled. So weights reach at most
 // 2^15 in fp16 and lose bits only 2^-(14 + kLift) below the reference.
-// The sum of weights without value scales adds w * 2^-lg. lg stops at kLgMin, which
-// also stands for blocks of zeros: such weights are far below every other's, yet
-// their part of that sum is kept wherever it matters (2^-34 of it is lost at most).
-constexpr float kLift = 8.f, kSlack = 7.f, kLgMin = -100.f;
+// The sum of weights without value scales adds w * 2^-lg.
+// Blocks of zeros take lg = kLgZero: such weights are far below every other's, yet their part of
+// that sum is kept wherever it matters (2^-54 of it is lost at most) and does not overflow it.
+// Where value scales are further apart than 2^kLgWide, the smaller blocks' weights have no bits beside those of a
+// block whose codes are zeros next to one large value (in another column, or not seen). Such items are
+// wide and go row by row through plain_row. (2^24 apart, 2^-33 of the larger is 2^-9 of the smaller: bf16's rounding.)
+constexpr float kLift = 8.f, kSlack = 7.f, kLgZero = -80.f, kLgWide = -24.f;
 constexpr float kLog2e = 1.4426950408889634f;
 
 // One block's constants in shared memory.
 struct BlockScales {
     float ks;      // key scale; negative: the page is out of range, the block is not seen
-    float lg;      // log2(value scale / largest of the item), at least kLgMin (also where the scale is 0)
+    float lg;      // log2(value scale / largest of the item), kLgZero where the scale is 0
     float inv;     // 2^-lg
     int page;
 };

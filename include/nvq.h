@@ -444,7 +444,8 @@ size_t nv_kv_attention_workspace_size(nv_dtype dt, int64_t rows, int Hq, int H, 
  *         contents on entry do not matter; calls that share it must not overlap.
  * Sums and softmax statistics are fp32. A bf16 call of 64 or 128 values a head runs on
  * the tensor cores in fp16 (queries, scaled by a power of two, and codes are exact there,
- * softmax weights are rounded to 11 bits); other calls run in fp32. Routing and the
+ * softmax weights are rounded to 11 bits); other calls run in fp32, and so do the rows of such
+ * a call that meet value scales more than 2^24 apart (slowly). Routing and the
  * partition of long sequences follow from the sizes and each sequence's
  * length, so results are deterministic.
  */

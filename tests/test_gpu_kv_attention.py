@@ -487,3 +487,39 @@ def test_queries_and_values_at_the_ends_of_the_range(size, news, dtype, D, mode)
     room = R.attention_tolerance(out, terms, dtype, D, 300)
     err = (got.double() - out).abs()
     assert bool((err <= room).all()), float((err / room).max())
+
+
+@pytest.mark.parametrize("mode", ["int8", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("news,H,G,block,causal,window", [
+    (1, 2, 4, 64, True, 0), (3, 1, 4, 16, True, 0), (2, 2, 8, 32, True, 300), (1, 1, 16, 128, False, 0),  # few rows
+    (200, 1, 4, 64, True, 0), (90, 2, 1, 16, True, 250), (40, 1, 2, 128, False, 0), (700, 8, 8, 64, True, 0)])  # many; parts and one
+@pytest.mark.parametrize("size", [2.0 ** 20, 2.0 ** 27, 2.0 ** 60, 2.0 ** 110, 2.0 ** 124, 2.0 ** -20, 2.0 ** -60, 2.0 ** -110])
+def test_values_of_another_size(size, news, H, G, block, causal, window, D, mode):
+    """A cache written from values of about 1, but for a block of zeros, a token (or, where they are smaller,
+    a block) in the middle that weighs next to nothing, and the last token, which only the last row
+    sees. A large value leaves the other codes of its block 0. Rows that do not see it, or see another block's values
+    beside it, are as exact as ever: no room is left for the size of a block's scale, but what the
+    weights' 2^-33 of it are where it is at most 2^24 times another's."""
+    n = 700
+    whole, step = R.Step([n], [n], block, seed=15), R.Step([n], [news], block, seed=15)
+    g = torch.Generator().manual_seed(4)
+    k, v = (torch.randn(n, H, D, generator=g).double() for _ in range(2))
+    q = torch.randn(step.rows, H * G, D, generator=g).to(BF16)
+    mid = n // 2 + 5
+    v[block * 2: block * 3] = 0
+    if size > 1:
+        v[mid] *= size
+        k[:, :, 0], q[:, :, 0] = 0, 30
+        k[mid, :, 0] = -60
+    else:
+        v[mid // block * block: (mid // block + 1) * block] *= size
+    v[n - 1] *= size
+    zeros = torch.zeros(step.P, H, block, D, dtype=torch.uint8), torch.zeros(step.P, H)
+    caches = (*R.write(k.float(), *zeros, whole, mode), *R.write(v.float(), *zeros, whole, mode))
+    got = _run(step, q, caches, mode, causal=causal, window=window, max_q=news)
+    out, a, dz, small = R.attention(q, *caches, step, mode, D ** -0.5, causal, window)
+    near = 2.0 ** -24 <= size <= 2.0 ** 24
+    room = R.attention_tolerance(out, (a, dz, small if near else small * 0), BF16, D, n)
+    err = (got.double() - out).abs()
+    assert bool((err <= room).all()), float((err / room).max())
