@@ -66,7 +66,7 @@ def lib():
         if _LIB is None:
             path = _build.LIB
             if not os.path.exists(path):
-                _build.build()
+                _build.build(calls=False)
             if not os.path.exists(path):
                 raise RuntimeError(f"libnvq.so missing at {path}; the CUDA library is required")
             L = C.CDLL(path)

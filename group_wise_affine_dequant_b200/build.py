@@ -62,11 +62,10 @@ def build_calls() -> str:
 
 
 def stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(CALLS):
+    if not os.path.exists(LIB):
         return True
     t = os.path.getmtime(LIB)
-    return any(os.path.getmtime(f) > t for f in _sources() + _headers()) or \
-        os.path.getmtime(CALLS_SRC) > os.path.getmtime(CALLS)
+    return any(os.path.getmtime(f) > t for f in _sources() + _headers())
 
 
 def _compile(src: str, verbose: bool) -> str:
@@ -82,17 +81,23 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
-def build(verbose: bool = False) -> str:
+def _link(objs) -> None:
+    tmp = LIB + ".tmp"
+    subprocess.run([NVCC, *ARCH, "-shared", "-o", tmp, *objs], check=True)
+    os.replace(tmp, LIB)
+
+
+def build(verbose: bool = False, calls: bool = True) -> str:
+    """Build libnvq.so and, with `calls`, the extension. The library is in place whatever becomes of the
+    extension, which needs more of the machine (a C++20 compiler, the headers of Python and torch);
+    its error is raised behind it."""
     os.makedirs(BUILD, exist_ok=True)
     srcs = _sources()
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs)) + 1) as ex:
-        calls = ex.submit(build_calls)
-        objs = list(ex.map(lambda s: _compile(s, verbose), srcs))
-        calls.result()
-    tmp = LIB + ".tmp"
-    cmd = [NVCC, *ARCH, "-shared", "-o", tmp, *objs]
-    subprocess.run(cmd, check=True)
-    os.replace(tmp, LIB)
+        extension = ex.submit(build_calls) if calls else None
+        _link(list(ex.map(lambda s: _compile(s, verbose), srcs)))
+        if extension:
+            extension.result()
     return LIB
 
 
