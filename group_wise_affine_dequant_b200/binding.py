@@ -490,17 +490,18 @@ def _calls():
     that do not fit and returns the outputs, or the status of a refused call. Where a
     stream is given, outputs and workspaces are allocated on it, as under torch.cuda.stream."""
     global _CALLS
-    if _CALLS is None:
-        L = lib()
-        if not os.path.exists(_build.CALLS):
-            _build.build_calls()
-        spec = importlib.util.spec_from_file_location("_calls", _build.CALLS)
-        module = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(module)
-        module.bind(*(C.cast(f, C.c_void_p).value for f in (
-            L.nv_moe_route, L.nv_kv_quantize, L.nv_kv_dequantize, L.nv_kv_attention,
-            L.nv_kv_attention_workspace_size)))
-        _CALLS = module
+    L = lib()
+    with _LOCK:
+        if _CALLS is None:
+            if not os.path.exists(_build.CALLS):
+                _build.build_calls()
+            spec = importlib.util.spec_from_file_location("_calls", _build.CALLS)
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
+            module.bind(*(C.cast(f, C.c_void_p).value for f in (
+                L.nv_moe_route, L.nv_kv_quantize, L.nv_kv_dequantize, L.nv_kv_attention,
+                L.nv_kv_attention_workspace_size)))
+            _CALLS = module
     return _CALLS
 
 

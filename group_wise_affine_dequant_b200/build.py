@@ -48,7 +48,7 @@ def build_calls() -> str:
     home = os.path.dirname(torch.__file__)
     nvcc = shutil.which(NVCC)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc))) if nvcc else "/usr/local/cuda"
-    tmp = CALLS + ".tmp"
+    tmp = f"{CALLS}.{os.getpid()}.tmp"  # several processes may build at once
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++20", "-fPIC", "-shared", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f"-I{home}/include",
            f"-I{home}/include/torch/csrc/api/include", "-I" + sysconfig.get_paths()["include"], f"-I{cuda}/include",

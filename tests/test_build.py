@@ -1,6 +1,9 @@
 """Building and loading the two binaries: the C library and the extension module
 that marshals tensors into its serving calls (CPU only; no compiler runs here)."""
 import os
+import shutil
+import threading
+import time
 
 import pytest
 
@@ -33,3 +36,46 @@ def test_loading_the_library_builds_no_extension(elsewhere, monkeypatch):
     with pytest.raises(OSError):  # what the fixture links is no library
         B.lib()
     assert os.path.exists(build_module.LIB)
+
+
+def _copied_extension(monkeypatch, tmp_path):
+    """A missing extension whose build copies the real one; returns the list of its builds."""
+    real, builds = build_module.CALLS, []
+    if not os.path.exists(real):
+        build_module.build_calls()
+
+    def build_calls():
+        builds.append(threading.get_ident())
+        time.sleep(0.2)
+        shutil.copy(real, build_module.CALLS)
+        return build_module.CALLS
+
+    B.lib()
+    monkeypatch.setattr(build_module, "CALLS", str(tmp_path / "_calls.so"))
+    monkeypatch.setattr(build_module, "build_calls", build_calls)
+    monkeypatch.setattr(B, "_CALLS", None)
+    return builds
+
+
+def test_threads_that_call_first_build_once(monkeypatch, tmp_path):
+    builds, found = _copied_extension(monkeypatch, tmp_path), []
+    threads = [threading.Thread(target=lambda: found.append(B._calls())) for _ in range(6)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(builds) == 1 and len(found) == 6 and all(m is found[0] for m in found)
+
+
+def test_a_build_writes_to_a_file_of_its_process(monkeypatch):
+    """Ranks that build at the same time do not write into each other's file."""
+    commands = []
+
+    class Failed:
+        returncode, stderr = 1, "not run"
+
+    monkeypatch.setattr(build_module.subprocess, "run", lambda cmd, **kw: commands.append(cmd) or Failed)
+    with pytest.raises(RuntimeError, match="not run"):
+        build_module.build_calls()
+    out = commands[0][commands[0].index("-o") + 1]
+    assert out != build_module.CALLS and str(os.getpid()) in os.path.basename(out)
