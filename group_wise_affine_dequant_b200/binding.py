@@ -486,14 +486,14 @@ _CALLS = None
 
 def _calls():
     """The extension module that marshals the calls below (csrc/torch_calls.cpp), bound to
-    the loaded library; built first if it is missing. It raises ValueError for tensors
+    the loaded library; built first if it is missing, or of another torch, Python or source. It raises ValueError for tensors
     that do not fit and returns the outputs, or the status of a refused call. Where a
     stream is given, outputs and workspaces are allocated on it, as under torch.cuda.stream."""
     global _CALLS
     L = lib()
     with _LOCK:
         if _CALLS is None:
-            if not os.path.exists(_build.CALLS):
+            if not _build.calls_current():
                 _build.build_calls()
             spec = importlib.util.spec_from_file_location("_calls", _build.CALLS)
             module = importlib.util.module_from_spec(spec)

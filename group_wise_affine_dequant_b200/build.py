@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import hashlib
 import os
 import shutil
 import subprocess
@@ -41,8 +42,31 @@ CALLS_SRC = os.path.join(CSRC, "torch_calls.cpp")
 CALLS = os.path.join(HERE, "_calls.so")
 
 
+def _calls_key() -> str:
+    """What the extension depends on: its source, the C interface, torch and Python."""
+    import torch
+
+    key = hashlib.sha256(f"{torch.__version__} {sysconfig.get_config_var('SOABI')}".encode())
+    for path in (CALLS_SRC, os.path.join(INCLUDE, "nvq.h")):
+        with open(path, "rb") as f:
+            key.update(f.read())
+    return key.hexdigest()
+
+
+def _key_file() -> str:
+    return os.path.join(BUILD, "calls.key")
+
+
+def calls_current() -> bool:
+    """The extension is there and was built from these files against this torch and Python."""
+    if not os.path.exists(CALLS) or not os.path.exists(_key_file()):
+        return False
+    with open(_key_file()) as f:
+        return f.read() == _calls_key()
+
+
 def build_calls() -> str:
-    """Compile the extension module _calls."""
+    """Compile the extension module _calls, and note what it was built from."""
     import torch
 
     home = os.path.dirname(torch.__file__)
@@ -58,6 +82,10 @@ def build_calls() -> str:
     if r.returncode != 0:
         raise RuntimeError(f"{cmd[0]} failed on {CALLS_SRC}:\n{r.stderr}")
     os.replace(tmp, CALLS)
+    os.makedirs(BUILD, exist_ok=True)
+    with open(f"{_key_file()}.{os.getpid()}.tmp", "w") as f:
+        f.write(_calls_key())
+    os.replace(f.name, _key_file())
     return CALLS
 
 

@@ -2,10 +2,12 @@
 that marshals tensors into its serving calls (CPU only; no compiler runs here)."""
 import os
 import shutil
+import sysconfig
 import threading
 import time
 
 import pytest
+import torch
 
 from group_wise_affine_dequant_b200 import binding as B
 from group_wise_affine_dequant_b200 import build as build_module
@@ -79,3 +81,22 @@ def test_a_build_writes_to_a_file_of_its_process(monkeypatch):
         build_module.build_calls()
     out = commands[0][commands[0].index("-o") + 1]
     assert out != build_module.CALLS and str(os.getpid()) in os.path.basename(out)
+
+
+def test_an_extension_of_another_torch_python_or_source_is_built_again(monkeypatch, tmp_path):
+    """What is loaded was built from the present files against the present torch and Python."""
+    if not build_module.calls_current():
+        build_module.build_calls()
+    assert build_module.calls_current()
+    other = tmp_path / "torch_calls.cpp"
+    other.write_text(open(build_module.CALLS_SRC).read() + "// changed")
+    for change in ((torch, "__version__", "0.0"), (sysconfig, "get_config_var", lambda name: "cpython-00"),
+                   (build_module, "CALLS_SRC", str(other)), (build_module, "BUILD", str(tmp_path))):
+        with monkeypatch.context() as m:
+            m.setattr(*change)
+            assert not build_module.calls_current(), change
+            m.setattr(B, "_CALLS", None)
+            m.setattr(build_module, "build_calls", lambda: (_ for _ in ()).throw(RuntimeError("built again")))
+            with pytest.raises(RuntimeError, match="built again"):
+                B._calls()
+    assert build_module.calls_current()
