@@ -42,24 +42,26 @@ constexpr int kBlocksMax = kChunkMax / 16 + 1;
 
 constexpr int kCtas = 3;         // resident on an SM
 
-// Even: a stage then belongs to one pair of consumer warps for good, so that the parity
-// a pair waits for cannot be that of the stage's previous filling.
+// Even: within an item a stage then belongs to one pair of consumer warps, which frees a filling before it waits
+// for the next, so that the parity it waits for cannot be that of the filling before last. From item to
+// item a stage may change pairs (an item can have an odd number of them): there the barriers at an item's end, which all
+// consumers pass, put one pair's last wait before the other's first.
 template <int D>
 constexpr int kStages = D == 128 ? 4 : 8;
 static_assert(kStages<64> % 2 == 0 && kStages<128> % 2 == 0, "");
 
 struct ItemMeta {
     int64_t row0;       // first row of the sequence in the step
-    int64_t part;       // partial index of (row 0 of the tile, chunk 0), or -1: the item writes the output
     int h, s;
     int f0, rows;       // the tile's first flattened row (token * G + group head) and its rows
     int first;          // place of the sequence's first row
     int len;
     int t0, t1;         // tokens [t0, t1) of the chunk; t0 a multiple of 64
     int lo_max, hi_min; // tokens in [lo_max, hi_min) are visible to every row of the tile
-    int chunk, pstride; // partial index of row r: part + r * pstride (+ chunk)
+    int chunk;
     int block0;         // t0 / block
     float vmax;         // largest value scale of the item
+    bool direct;        // the sequence's only chunk: the item writes the output, else partials
     bool wide;          // value scales too far apart for fp16 weights: no stages, the rows go one by one
 };
 
@@ -131,7 +133,7 @@ __device__ __noinline__ void wide_item(const DecodeArgs& p, const ItemMeta& m, P
         const int64_t t = m.row0 + f / G;
         const PlainRow r = plain_row<NV_BF16, MODE>(p.a, p.c, p.st, m.s, span, t, hq, m.t0, m.t1, d, scratch,
                                                     [] { asm volatile("bar.sync 1, 128;" ::: "memory"); });
-        if (m.part < 0) {
+        if (m.direct) {
             if (d < D) static_cast<uint16_t*>(p.a.out)[(t * p.a.Hq + hq) * D + d] = f32_to_bf16_bits(r.out[0]);
         } else {
             const int64_t at = part_row(p, span, m.s, m.h, f) * p.max_chunks + m.chunk;
@@ -307,7 +309,7 @@ kv_attn_decode_kernel(const __grid_constant__ DecodeArgs p, const __grid_constan
             if (lane == 0) {
                 ItemMeta& m = meta[slot];
                 m.row0 = sw.span.row0;
-                m.part = sw.chunks > 1 ? part_row(p, sw.span, s, h, f0) : -1;
+                m.direct = sw.chunks == 1;
                 m.h = h;
                 m.s = s;
                 m.f0 = f0;
@@ -664,7 +666,7 @@ kv_attn_decode_kernel(const __grid_constant__ DecodeArgs p, const __grid_constan
                         x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
                     }
                     x.x *= inv; x.y *= inv; x.z *= inv; x.w *= inv;
-                    if (m.part < 0) {
+                    if (m.direct) {
                         uint16_t* out = static_cast<uint16_t*>(p.a.out) +
                                         ((m.row0 + f / G) * p.a.Hq + m.h * G + f % G) * D + d;
                         *reinterpret_cast<uint2*>(out) = make_uint2(tc::f2_to_bf2(x.x, x.y), tc::f2_to_bf2(x.z, x.w));
