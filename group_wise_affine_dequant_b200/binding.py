@@ -512,7 +512,9 @@ def nv_moe_route(logits: torch.Tensor, topk: int, score: str = "softmax",
     """(ids int32 [T, topk], weights fp32 [T, topk]) of router logits [T, E]: what
     nv_moe_swiglu takes as ids and rw. score 'softmax' or 'sigmoid'; bias fp32 [E]
     is added for the choice only; with groups > 1 only the topk_groups best groups
-    are chosen from (a group's score: its group_top = 1 or 2 largest, summed)."""
+    are chosen from (a group's score: its group_top = 1 or 2 largest, summed).
+    With stream, ids and weights that are not given are allocated on it (as under
+    torch.cuda.stream); so it is with the outputs and workspaces of the three calls below."""
     if score not in _ROUTE_SCORES:
         raise ValueError(f"score must be one of {sorted(_ROUTE_SCORES)}")
     r = (_CALLS or _calls()).moe_route(
@@ -542,7 +544,8 @@ def nv_kv_dequantize(k_codes: torch.Tensor, k_scales: torch.Tensor, v_codes: tor
                      flags: torch.Tensor | None = None, stream=None):
     """(k, v) [rows, H, D]: the last starts[s + 1] - starts[s] tokens of every
     sequence, read back (all of them where starts is the running sum of lens).
-    out: a pair of tensors to write to; rows of no sequence are left as they were."""
+    out: a pair of tensors to write to; rows of no sequence are left as they were. With
+    stream, outputs that are not given are allocated on it."""
     k, v = (None, None) if out is None else out
     r = (_CALLS or _calls()).kv_dequantize(
         k_codes, k_scales, v_codes, v_scales, pages, starts, lens, flags, rows, dtype, k, v,
@@ -568,7 +571,8 @@ def nv_kv_attention(q: torch.Tensor, k_codes: torch.Tensor, k_scales: torch.Tens
     paged 8-bit cache, which holds the step's own keys and values already. scale
     defaults to D ** -0.5; window > 0 limits a causal row to its last `window`
     tokens; max_q is the largest number of rows of one sequence, if known.
-    Returns out [rows, Hq, D]; rows of no sequence are left as they were."""
+    Returns out [rows, Hq, D]; rows of no sequence are left as they were. With stream, an
+    output and a workspace that are not given are allocated on it."""
     r = (_CALLS or _calls()).kv_attention(
         q, k_codes, k_scales, v_codes, v_scales, pages, starts, lens, flags, scale, causal, window, max_q, workspace,
         out, None if stream is None else _stream(stream))

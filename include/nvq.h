@@ -439,15 +439,16 @@ size_t nv_kv_attention_workspace_size(nv_dtype dt, int64_t rows, int Hq, int H, 
  *         q must be finite and its scores within fp32's range: a row that holds NaN or
  *         infinities, or whose scores overflow, gives no number and changes no other row.
  * max_q   the largest number of rows of one sequence if known, else 0: a hint
- *         that chooses kernels, results do not depend on its being right.
+ *         that chooses kernels; results are right, to rounding, whether it is or not.
  * workspace 16-byte aligned, nv_kv_attention_workspace_size(...) bytes; its
  *         contents on entry do not matter; calls that share it must not overlap.
  * Sums and softmax statistics are fp32. A bf16 call of 64 or 128 values a head runs on
  * the tensor cores in fp16 (queries, scaled by a power of two, and codes are exact there,
  * softmax weights are rounded to 11 bits); other calls run in fp32, and so do the rows of such
  * a call that meet value scales more than 2^24 apart (slowly). Routing and the
- * partition of long sequences follow from the sizes and each sequence's
- * length, so results are deterministic.
+ * partition of long sequences follow from the sizes, max_q, the GPU's number of SMs and each
+ * sequence's own length: results are deterministic, and in calls of the same sizes a sequence's rows
+ * do not depend on the other sequences. Alone, or in another batch, they may be summed in other parts.
  */
 nv_status nv_kv_attention(const void* q, int64_t q_stride, nv_dtype dt, int64_t rows, int Hq,
                           const uint8_t* k_codes, const float* k_scales, const uint8_t* v_codes,

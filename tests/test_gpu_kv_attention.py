@@ -523,3 +523,37 @@ def test_values_of_another_size(size, news, H, G, block, causal, window, D, mode
     room = R.attention_tolerance(out, (a, dz, small if near else small * 0), BF16, D, n)
     err = (got.double() - out).abs()
     assert bool((err <= room).all()), float((err / room).max())
+
+
+@pytest.mark.parametrize("D,mode", [(128, "int8"), (64, "e4m3"), (80, "int8")])
+@pytest.mark.parametrize("news", [[1, 1, 1], [40, 3, 20], [2, 300, 1]])
+def test_a_sequence_does_not_depend_on_its_neighbours(news, D, mode):
+    """In calls of the same sizes a sequence's rows are the same bits whatever the other sequences' lengths, contents
+    and places are. (Alone, or beside more or fewer, it may be cut into other parts.)"""
+    H, G, block, n = 2, 4, 64, 5000
+    first = R.Step([n, 300, 900], news, block, seed=16)
+    P, width = 400, first.pages.shape[1]
+    caches = [*_cache(P, H, block, D, mode, 1), *_cache(P, H, block, D, mode, 2)]
+    q = torch.randn(first.rows, H * G, D, generator=torch.Generator().manual_seed(1)).to(BF16)
+    want = _run(first, q, caches, mode, max_q=max(news))
+    spare = [p for p in range(P) if p not in set(first.pages[0].tolist())]
+    for place, others in ((0, [4000, 25]), (1, [700, 4900]), (2, [300, 64])):
+        order = [1, 2]
+        order.insert(place, 0)
+        lens = list(others)
+        lens.insert(place, n)
+        step = R.Step([max(a, news[b]) for a, b in zip(lens, order)], [news[b] for b in order], block, seed=17)
+        table = torch.full((3, width), -7, dtype=torch.int32)
+        table[place] = first.pages[0]
+        at = 0
+        for s in range(3):
+            if s != place:
+                k = -(-step.lens[s] // block)
+                table[s, :k] = torch.tensor(spare[at: at + k], dtype=torch.int32)
+                at += k
+        step.pages = table
+        rows = torch.randn(step.rows, H * G, D, generator=torch.Generator().manual_seed(20 + place)).to(BF16)
+        r0 = int(step.starts[place])
+        rows[r0: r0 + news[0]] = q[: news[0]]
+        got = _run(step, rows, caches, mode, max_q=max(news))
+        assert torch.equal(got[r0: r0 + news[0]], want[: news[0]]), place
