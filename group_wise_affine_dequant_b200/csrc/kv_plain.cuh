@@ -53,6 +53,10 @@ __device__ __forceinline__ PlainRow plain_row(const KvAttn& a, const KvCache& c,
     sync();
 #pragma unroll
     for (int i = 0; i < kPlainThreads / 32; ++i) top = max(top, __float_as_uint(x.red[0][i]));
+    if (top >= 0x7F800000u) {  // not finite: else scores of -infinity alone would pass for nothing seen
+        sync();                // before the scratch is another row's
+        return PlainRow{{NAN, NAN}, 0.f, NAN};
+    }
     uint32_t ex = top >> 23;
     ex = ex < 8u ? 8u : ex > 247u ? 247u : ex;  // both powers of two are normal numbers
     const float down = __uint_as_float((254u - ex) << 23), zc = a.scale * __uint_as_float(ex << 23);

@@ -557,3 +557,25 @@ def test_a_sequence_does_not_depend_on_its_neighbours(news, D, mode):
         rows[r0: r0 + news[0]] = q[: news[0]]
         got = _run(step, rows, caches, mode, max_q=max(news))
         assert torch.equal(got[r0: r0 + news[0]], want[: news[0]]), place
+
+
+@pytest.mark.parametrize("dtype,D", [(BF16, 128), (BF16, 64), (F32, 64), (BF16, 80)])
+@pytest.mark.parametrize("news", [1, 70])
+@pytest.mark.parametrize("what", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("far", [False, True])
+def test_an_infinite_query_gives_no_number(what, news, dtype, D, far):
+    """Also where every score becomes -infinity, as if nothing were seen; in every kernel, and where value scales are far apart."""
+    H, G, mode = 1, 4, "int8"
+    step = R.Step([150], [news], 64, seed=18)
+    caches = [*_cache(step.P, H, 64, D, mode, 1), *_cache(step.P, H, 64, D, mode, 2)]
+    caches[0][..., 3] = 5 if what < 0 else 251  # keys of the other sign there
+    if far:
+        caches[3][step.pages[0, 0]] *= 2.0 ** 60
+    q = torch.randn(step.rows, G, D, generator=torch.Generator().manual_seed(1)).to(dtype)
+    clean = _run(step, q, caches, mode, max_q=news)
+    assert bool(torch.isfinite(clean.float()).all())
+    q[0, 2, 3] = what
+    got = _run(step, q, caches, mode, max_q=news)
+    assert not bool(torch.isfinite(got[0, 2].float()).any())
+    got[0, 2] = clean[0, 2]
+    assert torch.equal(got, clean)
