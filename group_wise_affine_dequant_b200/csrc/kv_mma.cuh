@@ -56,12 +56,13 @@ __device__ __forceinline__ float exp2_approx(float x) {
 }
 
 // A query row's power of two: with ex = the biased exponent of its largest magnitude, q *
-// 2^(127 - ex) is below 2 and exact in fp16 down to 2^-24. The ends of bf16's range stop
-// where both powers of two are normal fp32 numbers: rows of 2^113 and more come out up to 2^15
-// (fp16 ends at 2^16), rows below 2^-119 as multiples of 2^-14, which their last bit is.
+// 2^(127 - ex) is below 2 and exact in fp16 down to 2^-24. Rows of 2^7 and more come out up to 2^15
+// (fp16 ends at 2^16) instead, so that what their scores get back times the scale of keys near the largest
+// number stays finite: where the codes beside such a key are 0, so are their scores. Rows below
+// 2^-119 come out as multiples of 2^-14, which their last bit is. Both powers of two are normal fp32 numbers.
 __device__ __forceinline__ uint32_t row_exponent(uint32_t max_abs_bits) {
     const uint32_t ex = max_abs_bits >> 23;
-    return ex < 8u ? 8u : ex > 240u ? 240u : ex;
+    return ex < 8u ? 8u : ex <= 133u ? ex : ex <= 147u ? 133u : ex <= 254u ? ex - 14u : 240u;
 }
 __device__ __forceinline__ float pow2_bits(uint32_t biased) { return __uint_as_float(biased << 23); }
 

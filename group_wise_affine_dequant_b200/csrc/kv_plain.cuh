@@ -4,8 +4,7 @@
 // over the row's visible tokens, 128 at a time with a running maximum and sum. A
 // thread computes one token's score, then owns values d, d + 128 of the output.
 // Everything is fp32, and stays in its range wherever scores and values do: queries are taken
-// times a power of two (the row's largest is then between 1 and 2) that the scores get back, and
-// what is kept of the output is its mean so far, no sum.
+// times a power of two that the scores get back, and what is kept of the output is its mean so far, no sum.
 #pragma once
 
 #include "kv.cuh"
@@ -58,7 +57,9 @@ __device__ __forceinline__ PlainRow plain_row(const KvAttn& a, const KvCache& c,
         return PlainRow{{NAN, NAN}, 0.f, NAN};
     }
     uint32_t ex = top >> 23;
-    ex = ex < 8u ? 8u : ex > 247u ? 247u : ex;  // both powers of two are normal numbers
+    // 2^7 and more: up to 2^100, so that what the scores get back times a large key scale stays finite; below
+    // 2^-119: both powers of two stay normal numbers
+    ex = ex < 8u ? 8u : ex <= 133u ? ex : ex <= 233u ? 133u : ex - 100u;
     const float down = __uint_as_float((254u - ex) << 23), zc = a.scale * __uint_as_float(ex << 23);
 #pragma unroll
     for (int i = 0; i < 2; ++i)

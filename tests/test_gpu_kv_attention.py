@@ -579,3 +579,26 @@ def test_an_infinite_query_gives_no_number(what, news, dtype, D, far):
     assert not bool(torch.isfinite(got[0, 2].float()).any())
     got[0, 2] = clean[0, 2]
     assert torch.equal(got, clean)
+
+
+@pytest.mark.parametrize("dtype,D", [(BF16, 128), (BF16, 64), (F32, 64), (BF16, 80)])
+@pytest.mark.parametrize("mode", ["int8", "e4m3"])
+@pytest.mark.parametrize("news", [2, 70])
+@pytest.mark.parametrize("size", [1.0, 500.0, 4000.0, 5e5])
+def test_a_key_of_the_largest_size_out_of_sight(size, news, mode, dtype, D):
+    """The last token's key is near the largest number, which leaves the other codes of its block 0: to the rows in
+    front of it, of queries large and small, those are scores of 0."""
+    H, G, n = 1, 4, 150
+    step = R.Step([n], [news], 64, seed=19)
+    caches = [*_cache(step.P, H, 64, D, mode, 1), *_cache(step.P, H, 64, D, mode, 2)]
+    last = int(step.pages[0, (n - 1) // 64])
+    caches[0][last] = 0
+    caches[0][last, :, (n - 1) % 64] = 100
+    caches[1][last] = 3.38e38 / R.LARGEST[mode]
+    caches[1][step.pages[0, :2].long()] /= size
+    q = (torch.randn(step.rows, G, D, generator=torch.Generator().manual_seed(1)) * size).to(dtype)
+    got = _run(step, q, caches, mode, max_q=news)[:-1]
+    out, *terms = R.attention(q, *caches, step, mode, D ** -0.5)
+    room = R.attention_tolerance(out, terms, dtype, D, n)[:-1]
+    err = (got.double() - out[:-1]).abs()
+    assert bool((err <= room).all()), float((err / room).max())
