@@ -31,10 +31,11 @@
 // kSlack, so rescaling O in TMEM is rare and the softmax warps do it themselves.
 //
 // Bound: neither the tensor core (38 % busy) nor the exponential unit (39 %), but the chain of
-// one subtile's step, about 4600 cycles for a pair of tiles: the products of both subtiles in
-// turn (1650), then a softmax of 2900, whose 128 exponentials a thread issue one in 8 cycles
-// at best (1024 of them) and in 12.7 as one warp a scheduler reaches. Measured at a prompt
-// of 8192 (32 heads over 8, D = 128), each slower than the 668 us (823 TFLOP/s) of this
+// one subtile's step, about 4600 cycles for a pair of tiles: its own products (825; the other subtile's
+// run under its softmax), then a softmax of 2900, whose 128 exponentials a thread issue one in 8 cycles
+// at best (1024 of them) and in 12.7 as one warp a scheduler reaches; some 900 cycles between them are
+// not accounted for. Measured at a prompt
+// of 8192 (32 heads over 8, D = 128), each slower than the 665 to 683 us (827 to 805 TFLOP/s, from GPU to GPU) of this
 // form: scores held in registers through an unrolled loop, four softmax warpgroups with two threads a row (745), an issuing warp a
 // subtile, a share of the exponentials as polynomials on the FMA pipe.
 #include <cstdint>

@@ -360,7 +360,8 @@ nv_status nv_moe_route(const void* logits, nv_dtype dt, int64_t T, int64_t E, co
  *           NV_KV_E4M3: E4M3 without infinities), scales fp32 [P, H];
  *           value = code * scale. K and V have a codes and a scales array each.
  * A page is a block of `block` tokens (16, 32, 64 or 128) of H heads of D
- * values (a multiple of 16 up to 256).
+ * values (a multiple of 16 up to 256). H is at most 1024, P * H below 2^31, S below 2^24. Scales are
+ * finite and not negative, codes of a scale of 0 are 0 (as nv_kv_quantize writes them).
  * The step descriptor, shared by the three calls (int32 device arrays):
  *   lens    [S]: tokens of each sequence, this step's included; at most max_pages * block and
  *           2^31 - 2^16 (what is longer is flagged and cut);
