@@ -42,12 +42,16 @@ CALLS_SRC = os.path.join(CSRC, "torch_calls.cpp")
 CALLS = os.path.join(HERE, "_calls.so")
 
 
+def _calls_sources():
+    return CALLS_SRC, os.path.join(INCLUDE, "nvq.h")
+
+
 def _calls_key() -> str:
     """What the extension depends on: its source, the C interface, torch and Python."""
     import torch
 
     key = hashlib.sha256(f"{torch.__version__} {sysconfig.get_config_var('SOABI')}".encode())
-    for path in (CALLS_SRC, os.path.join(INCLUDE, "nvq.h")):
+    for path in _calls_sources():
         with open(path, "rb") as f:
             key.update(f.read())
     return key.hexdigest()
@@ -58,8 +62,13 @@ def _key_file() -> str:
 
 
 def calls_current() -> bool:
-    """The extension is there and was built from these files against this torch and Python."""
-    if not os.path.exists(CALLS) or not os.path.exists(_key_file()):
+    """The extension is there and was built from these files against this torch and Python. Where its
+    sources are not there, nothing else could be built: then it is taken as it is."""
+    if not os.path.exists(CALLS):
+        return False
+    if not all(os.path.exists(path) for path in _calls_sources()):
+        return True
+    if not os.path.exists(_key_file()):
         return False
     with open(_key_file()) as f:
         return f.read() == _calls_key()

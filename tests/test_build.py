@@ -100,3 +100,14 @@ def test_an_extension_of_another_torch_python_or_source_is_built_again(monkeypat
             with pytest.raises(RuntimeError, match="built again"):
                 B._calls()
     assert build_module.calls_current()
+
+
+def test_an_extension_without_its_sources_is_taken_as_it_is(monkeypatch, tmp_path):
+    """A package that was copied without its sources has nothing to build from."""
+    extension = tmp_path / "_calls.so"
+    monkeypatch.setattr(build_module, "CALLS", str(extension))
+    monkeypatch.setattr(build_module, "CALLS_SRC", str(tmp_path / "torch_calls.cpp"))
+    monkeypatch.setattr(build_module, "BUILD", str(tmp_path / "_build"))
+    assert not build_module.calls_current()
+    extension.touch()
+    assert build_module.calls_current()
